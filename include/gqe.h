@@ -54,7 +54,8 @@ typedef enum {
     GQE_ERR_UNSUPPORTED = 2,
     GQE_ERR_CUDA = 3,
     GQE_ERR_DEVICE_TIMEOUT = 4,
-    GQE_ERR_SCRATCH_LIMIT = 5
+    GQE_ERR_SCRATCH_LIMIT = 5,
+    GQE_ERR_OUT_OF_PAGES = 6 /* device status only: gqe_page_plan */
 } gqe_status;
 
 typedef enum { GQE_F32 = 0, GQE_BF16 = 1 } gqe_dtype;
@@ -466,6 +467,118 @@ gqe_status gqe_route_train(const gqe_shape* s, const void* x, const void* W_r, c
 size_t gqe_aux_loss_workspace_bytes(const gqe_shape* s);
 gqe_status gqe_aux_loss(const gqe_shape* s, const float* logits, const int32_t* idx, float* loss, float* dlogits,
                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A serving step over a paged cache: gqe_page_plan, gqe_kv_append and
+ * gqe_attn_chunk_paged.
+ *
+ * Requests 0 .. n_seqs-1 each bring any number of new tokens (one for a decode,
+ * a chunk of a prompt, none) to a step.  Their rows are packed one request after
+ * another: request b owns rows cu_new[b] .. cu_new[b+1]-1 of x, Q, idx, gate
+ * and O, so the step is routed and projected as one sequence, with the shape
+ * B = 1, T = the rows of the packed tensors.  Rows from cu_new[n_seqs] to T are
+ * padding.  The pages hold the dense KV path (gist.science summary, "Chemin KV
+ * Dense") as gqe_attn_decode_paged reads it: logical row s of request b is row
+ * s % page_size of page block_table[b * max_blocks + s / page_size].
+ *
+ * gqe_page_plan -- block tables and slot maps from the requests' lengths, on
+ * the device (the page gives no counterpart; it goes with the paged cache).
+ *
+ *   rows             T, the rows of the packed tensors (0 or more)
+ *   page_size        a power of two, 1 .. 65536; num_pages * page_size < 2^31
+ *   lengths [n_seqs]     device int32: rows in each request's cache before the step
+ *   new_lens [n_seqs]    device int32: rows it brings, 0 or more; -1: the request
+ *                        has ended and its pages are given back
+ *   free_pages [num_pages]   device int32, in/out: a stack of free pages, entries
+ *                        0 .. free_count-1.  The pages of ended requests are pushed
+ *                        (requests, then blocks, ascending); then each new block
+ *                        (same order) takes the page on top.
+ *   free_count [1]       device int32
+ *   block_table [n_seqs, max_blocks]   device int32, in/out: the new blocks'
+ *                        entries are written, no others
+ *   lengths_out [n_seqs] device int32 out: rows after the step (0: ended)
+ *   free_count_out [1]   device int32 out
+ *   cu_new [n_seqs + 1]  device int32 out: prefix sums of the new rows
+ *   slots [rows]         device int32 out: page * page_size + row in page of each
+ *                        packed row, -1 for the padding; may be NULL if rows is 0
+ *   workspace            the status word (256 bytes)
+ * lengths and free_count are not written, so a repeated call with the same
+ * arguments gives the same result; the caller passes lengths_out and
+ * free_count_out to the next step.  A step that cannot be served is refused as
+ * a whole: GQE_ERR_OUT_OF_PAGES in the status word if the free pages do not
+ * suffice, GQE_ERR_INVALID_ARGUMENT for a negative length, new_lens below -1, a
+ * request longer than page_size * max_blocks, more new rows than `rows`, or a
+ * stack that would exceed num_pages.  Then cu_new is all 0, slots all -1,
+ * lengths_out and free_count_out repeat the inputs, and free_pages and
+ * block_table stay as they were.  An entry of free_pages or block_table outside
+ * [0, num_pages) is reported as GQE_ERR_INVALID_ARGUMENT and its rows get slot -1.
+ * 1 <= n_seqs <= 16384; more return GQE_ERR_UNSUPPORTED.
+ */
+gqe_status gqe_page_plan(int n_seqs, int rows, int page_size, int num_pages, int max_blocks, const int32_t* lengths,
+                         const int32_t* new_lens, int32_t* free_pages, const int32_t* free_count,
+                         int32_t* block_table, int32_t* lengths_out, int32_t* free_count_out, int32_t* cu_new,
+                         int32_t* slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gqe_kv_append -- write the step's new K/V rows to their slots in the pages.
+ *
+ *   s                the step's shape; B*T rows, g, d_h and dtype are used
+ *   K_new, V_new     device, dtype: row t is [g, d_h], dense, at t * k_stride (V:
+ *                    t * v_stride) elements, so that they may be slices of a fused
+ *                    projection's output; 16-byte aligned rows
+ *   slots [B*T]      device int32 (gqe_page_plan): -1 rows are not written; two
+ *                    rows must not share a slot; a slot of num_pages * page_size
+ *                    or more is reported as GQE_ERR_INVALID_ARGUMENT and skipped
+ *   K_pages, V_pages [num_pages, page_size, g, d_h]   device, dtype, in/out
+ *   workspace        the status word (256 bytes)
+ * Implemented cases: bf16 or fp32, g * d_h * element size a multiple of 16.
+ */
+gqe_status gqe_kv_append(const gqe_shape* s, const void* K_new, int64_t k_stride, const void* V_new, int64_t v_stride,
+                         const int32_t* slots, void* K_pages, void* V_pages, int num_pages, int page_size,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gqe_attn_chunk_paged -- routed attention of every request's new tokens over
+ * its paged cache, with an optional sliding window.
+ *
+ * The new rows are in the cache already (gqe_kv_append).  With n_b =
+ * cu_new[b+1] - cu_new[b], the i-th new token of request b sits at position
+ * p = lengths[b] - n_b + i and sees the keys s <= p (causal on positions, as
+ * gqe_attn_prefill); with window > 0 only those with s > p - window or
+ * s < sinks: the last `window` keys, its own included, and the first `sinks`.
+ * For each selected head j of group q_:
+ *   o = sum_s softmax_s(Q[t,j,:] . K[s,q_,:] / sqrt(d_h)) V[s,q_,:],  O[t,j,:] = gate * o
+ * and O[t,j,:] = 0 for the unselected heads; rows of O past cu_new[n_seqs] are
+ * not written.  With one token per request it is the decode step
+ * (gqe_attn_decode_paged without a window).
+ *
+ *   s                B must be 1, T = the rows of Q, idx, gate and O
+ *   Q, O [T, h, d_h], idx, gate [T, g, k] as for gqe_attn_prefill; a head outside
+ *                    its group is reported in the status word and its row skipped
+ *                    (a token's heads must differ, as the router picks them)
+ *   K_pages, V_pages, num_pages, page_size, block_table, max_blocks
+ *                    as for gqe_attn_decode_paged; page_size * max_blocks <= 2^30
+ *   cu_new [n_seqs + 1], lengths [n_seqs]   device int32: as gqe_page_plan writes
+ *                    cu_new and lengths_out.  A request with rows outside [0, T), or
+ *                    with a cache shorter than its new rows or longer than the block
+ *                    table, is reported as GQE_ERR_INVALID_ARGUMENT and skipped.
+ *   window           0: no window; else 1 or more
+ *   sinks            0 or more (read with a window only)
+ *   workspace        at least gqe_chunk_workspace_bytes(s) bytes; calls that share
+ *                    it are ordered on one stream (graphs that may run at the same
+ *                    time need one each)
+ * Only pages that hold a visible key are read: block-table entries of pages
+ * that the window has left may be stale.  Infinities and NaN in keys or values
+ * that a row does not see, and rows past a cache's length, do not reach it.
+ * The result is the same in every run (no atomics on values).
+ * Implemented cases: bf16 or fp32, d_h in {32, 64, 128}.
+ */
+size_t gqe_chunk_workspace_bytes(const gqe_shape* s);
+gqe_status gqe_attn_chunk_paged(const gqe_shape* s, const void* Q, const void* K_pages, const void* V_pages,
+                                int num_pages, int page_size, const int32_t* block_table, int max_blocks, int n_seqs,
+                                const int32_t* cu_new, const int32_t* lengths, int window, int sinks,
+                                const int32_t* idx, const float* gate, void* O, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /* Synchronise `stream`, read the workspace status word, reset it to zero and
  * return it (GQE_OK when no kernel reported a failure). */

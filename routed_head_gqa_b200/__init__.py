@@ -23,6 +23,7 @@ GQE_ERR_UNSUPPORTED = 2
 GQE_ERR_CUDA = 3
 GQE_ERR_DEVICE_TIMEOUT = 4
 GQE_ERR_SCRATCH_LIMIT = 5
+GQE_ERR_OUT_OF_PAGES = 6
 GQE_F32 = 0
 GQE_BF16 = 1
 
@@ -32,6 +33,7 @@ EXPORTED = ["gqe_chunk_count", "gqe_workspace_bytes", "gqe_workspace_init", "gqe
             "gqe_group_slots", "gqe_routed_qproj", "gqe_routed_oproj", "gqe_backward_workspace_bytes", "gqe_attn_prefill_backward",
             "gqe_route_backward", "gqe_route_train", "gqe_aux_loss_workspace_bytes", "gqe_aux_loss",
             "gqe_attn_prefill_train", "gqe_attn_prefill_backward_saved",
+           "gqe_page_plan", "gqe_kv_append", "gqe_chunk_workspace_bytes", "gqe_attn_chunk_paged",
             "gqe_get_device_status", "gqe_status_string"]
 
 
@@ -49,6 +51,7 @@ class GQEError(RuntimeError):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_I64 = ctypes.c_int64
 _lib_handle = None
 
 
@@ -86,6 +89,11 @@ def _load():
     lib.gqe_aux_loss.argtypes = [S, _P, _P, _P, _P, _P, _SZ, _P]
     lib.gqe_attn_prefill_train.argtypes = [S] + [_P] * 12 + [_SZ, _P]
     lib.gqe_attn_prefill_backward_saved.argtypes = [S] + [_P] * 16 + [_SZ, _P]
+    lib.gqe_page_plan.argtypes = [_I] * 5 + [_P] * 10 + [_SZ, _P]
+    lib.gqe_kv_append.argtypes = [S, _P, _I64, _P, _I64, _P, _P, _P, _I, _I, _P, _SZ, _P]
+    lib.gqe_chunk_workspace_bytes.argtypes = [S]
+    lib.gqe_chunk_workspace_bytes.restype = _SZ
+    lib.gqe_attn_chunk_paged.argtypes = [S, _P, _P, _P, _I, _I, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _SZ, _P]
     lib.gqe_get_device_status.argtypes = [_P, _P]
     lib.gqe_status_string.argtypes = [_I]
     lib.gqe_status_string.restype = ctypes.c_char_p
@@ -94,7 +102,8 @@ def _load():
               "gqe_attn_shared_head", "gqe_group_slots", "gqe_routed_qproj", "gqe_routed_oproj",
               "gqe_attn_decode_paged",
               "gqe_attn_prefill_backward", "gqe_route_backward", "gqe_get_device_status", "gqe_route_train",
-              "gqe_aux_loss", "gqe_attn_prefill_train", "gqe_attn_prefill_backward_saved"):
+              "gqe_aux_loss", "gqe_attn_prefill_train", "gqe_attn_prefill_backward_saved",
+              "gqe_page_plan", "gqe_kv_append", "gqe_attn_chunk_paged"):
         getattr(lib, f).restype = _I
     _lib_handle = lib
     return lib
@@ -129,6 +138,12 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _torch_stream(stream):
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream)
+    return stream  # a torch stream, or None: the current one
 
 
 def _nbytes(t):
@@ -279,6 +294,77 @@ def gqe_aux_loss(shape, logits, idx, loss, dlogits, workspace, stream=None) -> N
                                              _ptr(dlogits), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
+def _tensors(fn, *specs):
+    """Refuse (GQE_ERR_INVALID_ARGUMENT) a tensor that is not on the current
+    device, or not of the dtype, shape and dense layout the call reads it with.
+    specs: (tensor, dtype, shape)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t, dtype, shape in specs:
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.device.index != dev:
+            raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
+
+
+def _shape_dtype(shape: GqeShape):
+    return torch.bfloat16 if shape.dtype == GQE_BF16 else torch.float32
+
+
+def gqe_page_plan(page_size, lengths, new_lens, free_pages, free_count, block_table, lengths_out, free_count_out,
+                  cu_new, slots, workspace, stream=None) -> None:
+    """n_seqs, rows, num_pages and max_blocks are the sizes of lengths, slots,
+    free_pages and block_table's rows."""
+    n, i32 = lengths.numel(), torch.int32
+    _tensors("gqe_page_plan", (lengths, i32, (n,)), (new_lens, i32, (n,)), (free_pages, i32, (free_pages.numel(),)),
+             (free_count, i32, (1,)), (block_table, i32, (n, block_table.shape[-1])), (lengths_out, i32, (n,)),
+             (free_count_out, i32, (1,)), (cu_new, i32, (n + 1,)), (slots, i32, (slots.numel(),)),
+             (workspace, torch.uint8, workspace.shape))
+    _check("gqe_page_plan", _lib.gqe_page_plan(
+        n, slots.numel(), int(page_size), free_pages.numel(), block_table.shape[1], lengths.data_ptr(),
+        new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), block_table.data_ptr(),
+        lengths_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream(stream)))
+
+
+def gqe_kv_append(shape, K_new, V_new, slots, K_pages, V_pages, workspace, stream=None) -> None:
+    """K_new and V_new [rows, g, d_h] may have any row stride that keeps rows
+    16-byte aligned (slices of a fused projection's output)."""
+    fn, dt, g, d = "gqe_kv_append", _shape_dtype(shape), shape.g, shape.d_h
+    rows = shape.B * shape.T
+    _tensors(fn, (slots, torch.int32, (rows,)), (K_pages, dt, (*K_pages.shape[:2], g, d)), (V_pages, dt, K_pages.shape),
+             (workspace, torch.uint8, workspace.shape))
+    for t in (K_new, V_new):
+        if (t.dtype != dt or t.shape != (rows, g, d) or t.stride(2) != 1 or (g > 1 and t.stride(1) != d)
+                or t.device != slots.device):
+            raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
+    _check(fn, _lib.gqe_kv_append(ctypes.byref(shape), K_new.data_ptr(), K_new.stride(0), V_new.data_ptr(),
+                                  V_new.stride(0), slots.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
+                                  K_pages.shape[0], K_pages.shape[1], workspace.data_ptr(), workspace.numel(),
+                                  _stream(stream)))
+
+
+def gqe_chunk_workspace_bytes(shape) -> int:
+    return int(_lib.gqe_chunk_workspace_bytes(ctypes.byref(shape)))
+
+
+def gqe_attn_chunk_paged(shape, Q, K_pages, V_pages, block_table, cu_new, lengths, window, sinks, idx, gate, O,
+                         workspace, stream=None) -> None:
+    """n_seqs, max_blocks, num_pages and page_size are the sizes of lengths,
+    block_table's rows and K_pages; tensors may carry a leading batch of 1."""
+    fn, dt, T, g, d = "gqe_attn_chunk_paged", _shape_dtype(shape), shape.T, shape.g, shape.d_h
+    n, i32 = lengths.numel(), torch.int32
+    rows = (T, shape.h, d) if Q.dim() == 3 else (1, T, shape.h, d)
+    sel = (T, g, shape.k) if idx.dim() == 3 else (1, T, g, shape.k)
+    _tensors(fn, (Q, dt, rows), (O, dt, O.shape if O.numel() == Q.numel() else rows), (idx, i32, sel),
+             (gate, torch.float32, gate.shape if gate.numel() == idx.numel() else sel),
+             (K_pages, dt, (*K_pages.shape[:2], g, d)), (V_pages, dt, K_pages.shape),
+             (block_table, i32, (n, block_table.shape[-1])), (cu_new, i32, (n + 1,)), (lengths, i32, (n,)),
+             (workspace, torch.uint8, workspace.shape))
+    _check(fn, _lib.gqe_attn_chunk_paged(
+        ctypes.byref(shape), Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), K_pages.shape[0], K_pages.shape[1],
+        block_table.data_ptr(), block_table.shape[1], n, cu_new.data_ptr(), lengths.data_ptr(), int(window),
+        int(sinks), idx.data_ptr(), gate.data_ptr(), O.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _stream(stream)))
+
+
 def gqe_get_device_status(workspace, stream=None) -> int:
     return _lib.gqe_get_device_status(_ptr(workspace), _stream(stream))
 
@@ -371,6 +457,60 @@ class Buffers:
 
     def backward_status(self, stream=None) -> int:
         return gqe_get_device_status(self._bwd[4], stream)
+
+    def status(self, stream=None) -> int:
+        return gqe_get_device_status(self.workspace, stream)
+
+
+class PagedCache:
+    """The paged K/V cache of up to n_seqs requests over some layers, and the
+    plan of the current step.  shape: the step's packed shape (B = 1, T = the
+    most new rows a step brings).  All state stays on the device at fixed
+    addresses, so a step can be captured into a graph and replayed:
+
+        cache.plan(new_lens)                      # pages and slots of the step
+        cache.append(K_new, V_new, layer)         # its rows into the pages
+        cache.attend(Q, idx, gate, O, layer)      # routed attention over the cache
+    """
+
+    def __init__(self, shape: GqeShape, n_seqs: int, num_pages: int, page_size: int, max_blocks: int, layers: int = 1,
+                 device="cuda"):
+        self.shape, self.page_size = shape, int(page_size)
+        dt = _shape_dtype(shape)
+        i32 = dict(dtype=torch.int32, device=device)
+        pages = (num_pages, page_size, shape.g, shape.d_h)
+        self.K_pages = [torch.empty(pages, dtype=dt, device=device) for _ in range(layers)]
+        self.V_pages = [torch.empty(pages, dtype=dt, device=device) for _ in range(layers)]
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)
+        self.block_table = torch.full((n_seqs, max_blocks), -1, **i32)
+        # lengths and the free page count, before and after the step's plan
+        self._before = torch.zeros(n_seqs + 1, **i32)
+        self._after = torch.zeros(n_seqs + 1, **i32)
+        self._after[n_seqs] = num_pages
+        self.lengths, self.free_count = self._after[:n_seqs], self._after[n_seqs:]
+        self.cu_new = torch.zeros(n_seqs + 1, **i32)
+        self.slots = torch.full((shape.T,), -1, **i32)
+        nbytes = gqe_chunk_workspace_bytes(shape)
+        if nbytes == 0:
+            raise GQEError("gqe_chunk_workspace_bytes", GQE_ERR_INVALID_ARGUMENT)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        gqe_workspace_init(self.workspace)
+
+    def plan(self, new_lens, stream=None):
+        """Start a step: new_lens [n_seqs] int32 on the device (-1 ends a request)."""
+        n = self._before.numel() - 1
+        with torch.cuda.stream(_torch_stream(stream)):
+            self._before.copy_(self._after)
+        gqe_page_plan(self.page_size, self._before[:n], new_lens, self.free_pages, self._before[n:], self.block_table,
+                      self.lengths, self.free_count, self.cu_new, self.slots, self.workspace, stream)
+
+    def append(self, K_new, V_new, layer=0, stream=None):
+        gqe_kv_append(self.shape, K_new, V_new, self.slots, self.K_pages[layer], self.V_pages[layer], self.workspace,
+                      stream)
+
+    def attend(self, Q, idx, gate, O, layer=0, window=0, sinks=0, stream=None):
+        gqe_attn_chunk_paged(self.shape, Q, self.K_pages[layer], self.V_pages[layer], self.block_table, self.cu_new,
+                             self.lengths, window, sinks, idx, gate, O, self.workspace, stream)
 
     def status(self, stream=None) -> int:
         return gqe_get_device_status(self.workspace, stream)

@@ -1,0 +1,460 @@
+// chunk_simt.cu -- routed attention of ragged chunks of new tokens over a paged
+// cache on the CUDA cores (every type and head width), and the merge of the
+// partial units.  See chunk.cuh for the units and the schedule.
+//
+// Per unit: up to 64 query rows, 64 keys a step, one pass over the keys with the
+// running row maximum and sum (S = Q K^T, P = 2^(S c - m), O += P V, rescaled
+// when the maximum grows).  256 threads as 16 x 16: thread (ty, tx) holds rows
+// ty + 16 i and keys tx + 16 j of S, and rows ty + 16 i of O, so a row's P is
+// written and read by one half warp.  A unit of at most 16 rows (a decode)
+// computes one row per thread instead of four.  K and V have one buffer each:
+// the copy of the next K runs under the softmax and P V, that of the next V under
+// the next S.
+#include "chunk.cuh"
+
+namespace gqe {
+namespace {
+
+constexpr int kBM = 64, kBN = 64, kThreads = 256;
+constexpr int kPStride = kBN + 4;
+
+template <typename T, int D>
+struct SimtCfg {
+    static constexpr int kVec = 16 / sizeof(T);           // elements per 16 bytes
+    static constexpr int kKV = D + kVec;                  // K/V row stride: rows 16 bytes apart modulo the banks
+    static constexpr int kQ = D + 4;
+    static constexpr size_t kSmem = sizeof(float) * (kBM * kQ + kBM * kPStride) + 2 * sizeof(T) * kBN * kKV;
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// One tile of K or V rows; keys that no row of the unit sees are zeros.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(const ChunkGeom& u, const ChunkItem& it, int step, const T* pages, T* dst) {
+    using C = SimtCfg<T, D>;
+    constexpr int kPer = D / C::kVec;  // 16-byte vectors per row
+    const int k0 = it.tile(step) * kBN;
+    for (int v = threadIdx.x; v < kBN * kPer; v += kThreads) {
+        const int row = v / kPer, x = (v % kPer) * C::kVec, s = k0 + row;
+        const bool on = s < it.hi && (s >= it.lo || s < u.sinks);
+        const T* src = pages;
+        if (on) src += (chunk_cache_row(u, it.b, s) * u.g + it.q) * D + x;
+        cp_async16(dst + row * C::kKV + x, src, on);
+    }
+}
+
+// N (2 or 4) consecutive elements, to fp32 and back.
+__device__ __forceinline__ void load_cols(const float* p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void load_cols(const float* p, float (&f)[2]) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    f[0] = v.x, f[1] = v.y;
+}
+__device__ __forceinline__ void load_cols(const __nv_bfloat16* p, float (&f)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load_cols(const __nv_bfloat16* p, float (&f)[2]) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    f[0] = __uint_as_float(v << 16), f[1] = __uint_as_float(v & 0xffff0000u);
+}
+__device__ __forceinline__ void store_cols(float* p, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store_cols(float* p, const float (&f)[2]) {
+    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+}
+__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&f)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+}
+__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&f)[2]) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
+}
+
+struct SimtShared {
+    ChunkSplit split;
+    ChunkItem item;
+    int has;
+    int row_j[kBM];
+};
+
+template <typename T, int D, int NR>
+__device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it, const SimtShared& sh, const T* Q,
+                                         const T* Kp, const T* Vp, T* O, float scale_log2, float* Qs, float* Ps, T* Ks,
+                                         T* Vs) {
+    using C = SimtCfg<T, D>;
+    constexpr int kVec = C::kVec;
+    constexpr int kCols = D / 16, kCW = kCols < 4 ? kCols : 4, kCN = kCols / kCW;  // O columns per thread
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int rows = it.nt * u.k;
+
+    load_tile<T, D>(u, it, it.s0, Kp, Ks);
+    cp_async_commit();
+    load_tile<T, D>(u, it, it.s0, Vp, Vs);
+    cp_async_commit();
+    // Q rows as fp32 (rows past the unit's, or of a bad selection, as zeros)
+    for (int v = tid; v < NR * 16 * (D / kVec); v += kThreads) {
+        const int r = v / (D / kVec), x = (v % (D / kVec)) * kVec;
+        float f[kVec];
+        if (r < rows && sh.row_j[r] >= 0) {
+            const int token = it.t0 + r / u.k;
+            unpack16(*reinterpret_cast<const uint4*>(Q + ((int64_t)token * u.h + sh.row_j[r]) * D + x), f, (const T*)nullptr);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) f[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; e += 4)
+            *reinterpret_cast<float4*>(Qs + r * C::kQ + x + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    }
+    // the unit's unselected output slots, by the part that holds its first step
+    if (it.s0 == 0) {
+        constexpr int kPer = D / kVec;
+        for (int v = tid; v < it.nt * u.hpg * kPer; v += kThreads) {
+            const int x = v % kPer, j = it.q * u.hpg + (v / kPer) % u.hpg, i = v / kPer / u.hpg;
+            bool chosen = false;
+            for (int r = 0; r < u.k; ++r) chosen |= sh.row_j[i * u.k + r] == j;
+            if (!chosen)
+                *reinterpret_cast<uint4*>(O + ((int64_t)(it.t0 + i) * u.h + j) * D + x * kVec) = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    float m[NR], l[NR], acc[NR][kCols];
+    int pos[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        const int r = ty + 16 * i;
+        pos[i] = r < rows ? it.p0 + r / u.k : -1;  // -1: sees nothing
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) acc[i][e] = 0.f;
+    }
+
+    for (int st = it.s0; st < it.s1; ++st) {
+        cp_async_wait<1>();  // K of this step
+        __syncthreads();
+        float s[NR][4];
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 2
+        for (int x = 0; x < D; x += kVec) {
+            float kf[4][kVec];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                unpack16(*reinterpret_cast<const uint4*>(Ks + (tx + 16 * j) * C::kKV + x), kf[j], (const T*)nullptr);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+#pragma unroll
+                for (int e = 0; e < kVec; e += 4) {
+                    const float4 qf = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * C::kQ + x + e);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i][j] = fmaf(qf.x, kf[j][e], s[i][j]);
+                        s[i][j] = fmaf(qf.y, kf[j][e + 1], s[i][j]);
+                        s[i][j] = fmaf(qf.z, kf[j][e + 2], s[i][j]);
+                        s[i][j] = fmaf(qf.w, kf[j][e + 3], s[i][j]);
+                    }
+                }
+            }
+        }
+        __syncthreads();  // every thread has read K
+        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Kp, Ks);
+        cp_async_commit();
+        const int k0 = it.tile(st) * kBN;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = chunk_sees(u, pos[i], k0 + tx + 16 * j) ? s[i][j] * scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m[i], mx);
+            const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen so far: every weight 0
+            const float corr = fast_exp2(m[i] - ref);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w = fast_exp2(s[i][j] - ref);
+                sum += w;
+                Ps[(ty + 16 * i) * kPStride + tx + 16 * j] = w;
+            }
+            l[i] = l[i] * corr + sum;  // this thread's keys; summed over the half warp at the end
+            m[i] = mn;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) acc[i][e] *= corr;
+        }
+        __syncwarp();
+        cp_async_wait<1>();  // V of this step
+        __syncthreads();
+#pragma unroll 2
+        for (int key = 0; key < kBN; key += 4) {
+            float4 pf[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) pf[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * kPStride + key);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                float vf[kCN][kCW];
+#pragma unroll
+                for (int cn = 0; cn < kCN; ++cn)
+                    load_cols(Vs + (key + kk) * C::kKV + cn * 16 * kCW + tx * kCW, vf[cn]);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const float w = kk == 0 ? pf[i].x : kk == 1 ? pf[i].y : kk == 2 ? pf[i].z : pf[i].w;
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e) acc[i][e] = fmaf(w, vf[e / kCW][e % kCW], acc[i][e]);
+                }
+            }
+        }
+        __syncthreads();  // every thread has read V
+        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Vp, Vs);
+        cp_async_commit();
+    }
+
+    const bool partial = chunk_partial(it);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        float sum = l[i];
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const int r = ty + 16 * i;
+        const int j = r < rows ? sh.row_j[r] : -1;
+        const bool none = m[i] == -INFINITY && sum == 0.f;
+        const float inv = none && partial ? 0.f : 1.f / sum;
+        float check = 0.f;
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) check += acc[i][e] * 0.f;  // 0, or NaN when a value is not finite
+        const bool bad = j >= 0 && !(check + sum * 0.f == 0.f);
+        unsigned again = __ballot_sync(0xffffffffu, bad);
+        const bool redo = (again & (0xffffu << (tid & 16))) != 0;  // a value of this half warp's row
+        if (j >= 0 && !redo) {
+            const int token = it.t0 + r / u.k;
+            float* rec = partial ? u.part + ((int64_t)chunk_slot(it, blockIdx.x) * u.row_cap + r) * (D + 4) : nullptr;
+            T* o = O + ((int64_t)token * u.h + j) * D;
+            const float f = partial ? inv : u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] * inv;
+#pragma unroll
+            for (int cn = 0; cn < kCN; ++cn) {
+                float out[kCW];
+#pragma unroll
+                for (int e = 0; e < kCW; ++e) out[e] = acc[i][cn * kCW + e] * f;
+                const int col = cn * 16 * kCW + tx * kCW;
+                if (partial)
+                    store_cols(rec + col, out);
+                else
+                    store_cols(o + col, out);
+            }
+            if (partial && tx == 0) rec[D] = none ? -INFINITY : m[i] + log2f(sum);
+        }
+        if (again != 0) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (!(again & (0xffffu << (16 * half)))) continue;
+                const int rr = ((tid >> 5) * 2 + half) + 16 * i;  // the half warp's row
+                const int jj = sh.row_j[rr], token = it.t0 + rr / u.k;
+                float a2[D / 32], m2, l2;
+                chunk_row<T, D>(u, it, it.p0 + rr / u.k, Q + ((int64_t)token * u.h + jj) * D, Kp, Vp, scale_log2, a2, m2, l2);
+                chunk_store_row<T, D>(u, it, blockIdx.x, rr, token, jj, a2, m2, l2, O);
+            }
+        }
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+chunk_simt_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
+                  T* __restrict__ O, float scale_log2) {
+    using C = SimtCfg<T, D>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ SimtShared sh;
+    float* Qs = reinterpret_cast<float*>(smem);
+    float* Ps = Qs + kBM * C::kQ;
+    T* Ks = reinterpret_cast<T*>(Ps + kBM * kPStride);
+    T* Vs = Ks + kBN * C::kKV;
+    const int tid = threadIdx.x;
+
+    chunk_split(u, sh.split, blockIdx.x, gridDim.x);
+    if (tid == 0) u.desc[2 * blockIdx.x].valid = u.desc[2 * blockIdx.x + 1].valid = 0;
+    ChunkWalk walk(sh.split);
+    while (true) {
+        if (tid == 0) {
+            sh.has = walk.next(u, sh.item);
+            if (sh.has && chunk_partial(sh.item)) chunk_describe(u, sh.item, blockIdx.x);
+        }
+        __syncthreads();
+        if (!sh.has) break;
+        const ChunkItem it = sh.item;
+        const int rows = it.nt * u.k;
+        for (int r = tid; r < rows; r += kThreads) sh.row_j[r] = chunk_head(u, it.t0 + r / u.k, it.q, r % u.k);
+        __syncthreads();
+        if (rows <= 16)
+            run_item<T, D, 1>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+        else
+            run_item<T, D, 4>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+        __syncthreads();  // the item, its row table and tiles may be overwritten
+    }
+    cp_async_wait<0>();
+}
+
+// Merge of a split unit: O = gate * sum_p 2^(lse_p - M) o_p / sum_p 2^(lse_p - M)
+// over its parts in order (reproducible).  Block (c, y) takes the unit whose
+// first steps part c holds (its slot 2c + 1), one warp per row, rows y apart.
+constexpr int kCombineWarps = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kCombineWarps)
+chunk_combine_kernel(const ChunkGeom u, int parts, T* __restrict__ O) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kRec = D + 4, kPer = D / 32;
+    __shared__ int16_t list[kChunkMaxParts];  // the unit's slots in order
+    __shared__ int count;
+    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const ChunkDesc d = u.desc[2 * c + 1];
+    if (!d.valid || d.s1 == d.steps) return;
+    if (warp == 0) {
+        int n = 1;
+        if (lane == 0) list[0] = (int16_t)(2 * c + 1);
+        for (int p0 = c + 1; p0 < parts; p0 += 32) {
+            const int p = p0 + lane;
+            bool mine = false, other = false;
+            if (p < parts) {
+                const ChunkDesc e = u.desc[2 * p];
+                mine = e.valid && e.q == d.q && e.t0 == d.t0 && e.b == d.b;
+                other = e.valid && !mine;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, mine), out = __ballot_sync(0xffffffffu, other);
+            if (mine) list[n + __popc(in & ((1u << lane) - 1u))] = (int16_t)(2 * p);
+            n += __popc(in);
+            if (out) break;  // a later unit's part: this unit's are all behind
+        }
+        if (lane == 0) count = n;
+    }
+    __syncthreads();
+    const int n = count, rows = d.nt * u.k;
+    for (int r = blockIdx.y * kCombineWarps + warp; r < rows; r += gridDim.y * kCombineWarps) {
+        const int token = d.t0 + r / u.k, slot = r % u.k;
+        const int j = u.idx[((int64_t)token * u.g + d.q) * u.k + slot];
+        if (j < d.q * u.hpg || j >= (d.q + 1) * u.hpg) continue;
+        float M = -INFINITY;
+        bool nan = false;
+        for (int i = lane; i < n; i += 32) {
+            const float x = u.part[((int64_t)list[i] * u.row_cap + r) * kRec + D];
+            M = fmaxf(M, x);
+            nan |= x != x;
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        if (__any_sync(0xffffffffu, nan)) M = NAN;
+        float L = 0.f, acc[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float* rec = u.part + ((int64_t)list[i] * u.row_cap + r) * kRec;
+            const float lse = rec[D];
+            if (lse == -INFINITY) continue;  // this part holds no key of the row
+            const float w = fast_exp2(lse - M);
+            L += w;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(rec[e * 32 + lane], w, acc[e]);
+        }
+        const float f = u.gate[((int64_t)token * u.g + d.q) * u.k + slot] / L;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            O[((int64_t)token * u.h + j) * D + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
+    }
+}
+
+int device_sms() {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    return sms;
+}
+
+size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
+
+int simt_parts() {
+    const int p = 2 * device_sms();
+    return p < kChunkMaxParts ? p : kChunkMaxParts;
+}
+
+ChunkGeom make_geom(const ChunkArgs& a, int bm, int bn, int parts) {
+    const gqe_shape& s = *a.s;
+    ChunkGeom u;
+    u.T = s.T;
+    u.n_seqs = a.n_seqs;
+    u.h = s.h;
+    u.g = s.g;
+    u.k = s.k;
+    u.hpg = s.h / s.g;
+    u.WU = bm / s.k;
+    u.BN = bn;
+    u.unit_keys = 2 * bn;
+    u.min_cost = 4 * bn;
+    u.row_cap = (int64_t)s.T * s.k < bm ? s.T * s.k : bm;
+    u.cap = a.max_blocks << a.page_shift;
+    u.window = a.window >= u.cap ? 0 : a.window;
+    u.sinks = u.window ? a.sinks : 0;
+    u.page_shift = a.page_shift;
+    u.num_pages = a.num_pages;
+    u.max_blocks = a.max_blocks;
+    u.cu = a.cu_new;
+    u.lengths = a.lengths;
+    u.block_table = a.block_table;
+    u.idx = a.idx;
+    u.gate = a.gate;
+    u.status = a.status;
+    u.desc = static_cast<ChunkDesc*>(a.scratch);
+    u.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) + a256(2 * parts * sizeof(ChunkDesc)));
+    return u;
+}
+
+template <typename T, int D>
+cudaError_t launch_simt(const ChunkArgs& a) {
+    const int parts = simt_parts();
+    const ChunkGeom u = make_geom(a, kBM, kBN, parts);
+    const size_t smem = SimtCfg<T, D>::kSmem;
+    cudaError_t err = cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+    chunk_simt_kernel<T, D><<<parts, kThreads, smem, a.stream>>>(u, (const T*)a.Q, (const T*)a.K_pages,
+                                                                 (const T*)a.V_pages, (T*)a.O, scale_log2);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    chunk_combine_kernel<T, D><<<dim3(parts, 2), 32 * kCombineWarps, 0, a.stream>>>(u, parts, (T*)a.O);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t chunk_scratch_bytes(const gqe_shape* s) {
+    const int64_t rows = (int64_t)s->T * s->k < kBM ? (int64_t)s->T * s->k : kBM;
+    const size_t parts = (size_t)simt_parts();
+    return a256(2 * parts * sizeof(ChunkDesc)) + a256(2 * parts * rows * (s->d_h + 4) * sizeof(float));
+}
+
+cudaError_t launch_chunk(const ChunkArgs& a) {
+    const bool bf = a.s->dtype == GQE_BF16;
+    switch (a.s->d_h) {
+        case 32: return bf ? launch_simt<__nv_bfloat16, 32>(a) : launch_simt<float, 32>(a);
+        case 64: return bf ? launch_simt<__nv_bfloat16, 64>(a) : launch_simt<float, 64>(a);
+        case 128: return bf ? launch_simt<__nv_bfloat16, 128>(a) : launch_simt<float, 128>(a);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace gqe

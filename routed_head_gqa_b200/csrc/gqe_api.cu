@@ -3,6 +3,7 @@
 #include <cstring>
 
 #include "backward.cuh"
+#include "chunk.cuh"
 #include "common.cuh"
 
 using namespace gqe;
@@ -37,6 +38,14 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t route_scratch_bytes(const gqe_shape* s) {
     return align256((size_t)s->B * s->h * gqe_chunk_count(s->T) * sizeof(int32_t));
+}
+
+bool page_size_ok(int ps) { return ps >= 1 && ps <= (1 << 16) && (ps & (ps - 1)) == 0; }
+
+int log2_of(int n) {
+    int shift = 0;
+    while ((1 << shift) < n) ++shift;
+    return shift;
 }
 
 gqe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GQE_OK : GQE_ERR_CUDA; }
@@ -409,6 +418,116 @@ gqe_status gqe_attn_decode_paged(const gqe_shape* s, const void* q, const void* 
     return from_cuda(launch_decode(a));
 }
 
+gqe_status gqe_page_plan(int n_seqs, int rows, int page_size, int num_pages, int max_blocks, const int32_t* lengths,
+                         const int32_t* new_lens, int32_t* free_pages, const int32_t* free_count,
+                         int32_t* block_table, int32_t* lengths_out, int32_t* free_count_out, int32_t* cu_new,
+                         int32_t* slots, void* workspace, size_t workspace_bytes, void* stream) {
+    if (n_seqs < 1 || rows < 0 || num_pages < 1 || max_blocks < 1) return GQE_ERR_INVALID_ARGUMENT;
+    if (!page_size_ok(page_size)) return GQE_ERR_INVALID_ARGUMENT;
+    if (!lengths || !new_lens || !free_pages || !free_count || !block_table || !lengths_out || !free_count_out ||
+        !cu_new || (rows > 0 && !slots))
+        return GQE_ERR_INVALID_ARGUMENT;
+    if (n_seqs > kPlanMaxSeqs) return GQE_ERR_UNSUPPORTED;
+    if ((int64_t)num_pages * page_size >= ((int64_t)1 << 31) || (int64_t)max_blocks * page_size >= ((int64_t)1 << 31))
+        return GQE_ERR_UNSUPPORTED;
+    gqe_status st = check_workspace(workspace, workspace_bytes, kStatusBytes);
+    if (st != GQE_OK) return st;
+    PlanArgs a;
+    a.n_seqs = n_seqs;
+    a.rows = rows;
+    a.page_shift = log2_of(page_size);
+    a.num_pages = num_pages;
+    a.max_blocks = max_blocks;
+    a.lengths = lengths;
+    a.new_lens = new_lens;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.block_table = block_table;
+    a.lengths_out = lengths_out;
+    a.free_count_out = free_count_out;
+    a.cu_new = cu_new;
+    a.slots = slots;
+    a.status = workspace;
+    return from_cuda(launch_page_plan(a, (cudaStream_t)stream));
+}
+
+gqe_status gqe_kv_append(const gqe_shape* s, const void* K_new, int64_t k_stride, const void* V_new, int64_t v_stride,
+                         const int32_t* slots, void* K_pages, void* V_pages, int num_pages, int page_size,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    gqe_status st = check_shape(s);
+    if (st != GQE_OK) return st;
+    if (!K_new || !V_new || !slots || !K_pages || !V_pages || num_pages < 1 || !page_size_ok(page_size))
+        return GQE_ERR_INVALID_ARGUMENT;
+    const int64_t elem = s->dtype == GQE_BF16 ? 2 : 4, row = (int64_t)s->g * s->d_h;
+    const int64_t rows = (int64_t)s->B * s->T;
+    if ((rows > 1 && (k_stride < row || v_stride < row)) || k_stride * elem % 16 != 0 || v_stride * elem % 16 != 0)
+        return GQE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(K_new) || !aligned16(V_new) || !aligned16(K_pages) || !aligned16(V_pages))
+        return GQE_ERR_INVALID_ARGUMENT;
+    if (row * elem % 16 != 0 || (int64_t)num_pages * page_size >= ((int64_t)1 << 31)) return GQE_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, workspace_bytes, kStatusBytes);
+    if (st != GQE_OK) return st;
+    AppendArgs a;
+    a.rows = rows;
+    a.k_stride = k_stride * elem;
+    a.v_stride = v_stride * elem;
+    a.row_bytes = row * elem;
+    a.K_new = static_cast<const char*>(K_new);
+    a.V_new = static_cast<const char*>(V_new);
+    a.slots = slots;
+    a.K_pages = K_pages;
+    a.V_pages = V_pages;
+    a.num_slots = (int64_t)num_pages * page_size;
+    a.status = workspace;
+    return from_cuda(launch_kv_append(a, (cudaStream_t)stream));
+}
+
+size_t gqe_chunk_workspace_bytes(const gqe_shape* s) {
+    if (check_shape(s) == GQE_ERR_INVALID_ARGUMENT) return 0;
+    return kStatusBytes + chunk_scratch_bytes(s);
+}
+
+gqe_status gqe_attn_chunk_paged(const gqe_shape* s, const void* Q, const void* K_pages, const void* V_pages,
+                                int num_pages, int page_size, const int32_t* block_table, int max_blocks, int n_seqs,
+                                const int32_t* cu_new, const int32_t* lengths, int window, int sinks,
+                                const int32_t* idx, const float* gate, void* O, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    gqe_status st = check_shape(s);
+    if (st != GQE_OK) return st;
+    if (s->B != 1 || num_pages < 1 || max_blocks < 1 || n_seqs < 1 || window < 0 || sinks < 0)
+        return GQE_ERR_INVALID_ARGUMENT;
+    if (!page_size_ok(page_size)) return GQE_ERR_INVALID_ARGUMENT;
+    if (!Q || !K_pages || !V_pages || !block_table || !cu_new || !lengths || !idx || !gate || !O)
+        return GQE_ERR_INVALID_ARGUMENT;
+    if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O)) return GQE_ERR_INVALID_ARGUMENT;
+    if (s->d_h != 32 && s->d_h != 64 && s->d_h != 128) return GQE_ERR_UNSUPPORTED;
+    if ((int64_t)page_size * max_blocks > ((int64_t)1 << 30) || (int64_t)num_pages * page_size >= ((int64_t)1 << 31))
+        return GQE_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, workspace_bytes, kStatusBytes + chunk_scratch_bytes(s));
+    if (st != GQE_OK) return st;
+    ChunkArgs a;
+    a.s = s;
+    a.Q = Q;
+    a.K_pages = K_pages;
+    a.V_pages = V_pages;
+    a.num_pages = num_pages;
+    a.page_shift = log2_of(page_size);
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.n_seqs = n_seqs;
+    a.cu_new = cu_new;
+    a.lengths = lengths;
+    a.window = window;
+    a.sinks = sinks;
+    a.idx = idx;
+    a.gate = gate;
+    a.O = O;
+    a.scratch = static_cast<char*>(workspace) + kStatusBytes;
+    a.status = workspace;
+    a.stream = (cudaStream_t)stream;
+    return from_cuda(launch_chunk(a));
+}
+
 size_t gqe_backward_workspace_bytes(const gqe_shape* s) {
     if (check_shape(s) == GQE_ERR_INVALID_ARGUMENT) return 0;
     const size_t a = attn_backward_scratch_bytes(s), r = route_backward_scratch_bytes(s);
@@ -571,6 +690,7 @@ const char* gqe_status_string(gqe_status s) {
         case GQE_ERR_CUDA: return "GQE_ERR_CUDA";
         case GQE_ERR_DEVICE_TIMEOUT: return "GQE_ERR_DEVICE_TIMEOUT";
         case GQE_ERR_SCRATCH_LIMIT: return "GQE_ERR_SCRATCH_LIMIT";
+        case GQE_ERR_OUT_OF_PAGES: return "GQE_ERR_OUT_OF_PAGES";
     }
     return "GQE_UNKNOWN_STATUS";
 }
