@@ -23,7 +23,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 LIB_SOURCES = ["gqe_api.cu", "router.cu", "router_tc.cu", "prefill_simt.cu", "prefill_tc.cu", "decode.cu",
                "output.cu", "qproj.cu", "proj_tc.cu", "backward.cu", "backward_tc.cu", "route_bwd.cu", "aux_loss.cu",
-               "paged.cu", "chunk_simt.cu"]
+               "paged.cu", "chunk.cu", "chunk_simt.cu",
+               "chunk_tc.cu"]
 SELFTEST_SOURCES = ["selftest.cu"]
 
 

@@ -37,7 +37,7 @@ struct ChunkDesc {
 
 struct ChunkGeom {
     int T, n_seqs, h, g, k, hpg;
-    int WU;           // tokens per unit
+    int W, WU;        // tokens per query tile and per unit
     int BN;           // keys per step
     int unit_keys;    // a unit's fixed cost, in keys
     int min_cost;     // smallest cost worth a part, in keys
@@ -281,7 +281,7 @@ __device__ __forceinline__ int chunk_head(const ChunkGeom& u, int token, int q, 
 // reaches rows that do not see the key; a row whose result is not finite is
 // therefore taken again here, where a key that the row does not see is not read.
 template <typename T, int D>
-__device__ __noinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& it, int p, const T* q_row, const T* Kp,
+__device__ __forceinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& it, int p, const T* q_row, const T* Kp,
                                        const T* Vp, float scale_log2, float (&acc)[D / 32], float& m, float& l) {
     const int lane = threadIdx.x & 31;
     float qv[D / 32];
@@ -294,23 +294,41 @@ __device__ __noinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& it, 
     l = 0.f;
     for (int st = it.s0; st < it.s1; ++st) {
         const int k0 = it.tile(st) * u.BN;
-        for (int s = k0; s < min(k0 + u.BN, p + 1); ++s) {
-            if (!chunk_sees(u, p, s)) continue;
-            const int64_t at = (chunk_cache_row(u, it.b, s) * u.g + it.q) * D;
-            float x = 0.f;
+        const int k1 = min(k0 + u.BN, p + 1);
+        for (int s = k0; s < k1; s += 4) {  // four keys' loads in flight
+            float x[4], v[4][D / 32];
+            bool on[4];
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) x = fmaf(qv[e], Elem<T>::to_f(Kp[at + e * 32 + lane]), x);
+            for (int j = 0; j < 4; ++j) {
+                on[j] = s + j < k1 && chunk_sees(u, p, s + j);
+                x[j] = 0.f;
+                if (on[j]) {
+                    const int64_t at = (chunk_cache_row(u, it.b, s + j) * u.g + it.q) * D;
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-            x *= scale_log2;
-            if (x == -INFINITY) continue;  // weight 0 beside any other key
-            const float mx = fmaxf(m, x);
-            const float corr = m == -INFINITY ? 0.f : fast_exp2(m - mx), w = fast_exp2(x - mx);
-            m = mx;
-            l = l * corr + w;
+                    for (int e = 0; e < D / 32; ++e) {
+                        x[j] = fmaf(qv[e], Elem<T>::to_f(Kp[at + e * 32 + lane]), x[j]);
+                        v[j][e] = Elem<T>::to_f(Vp[at + e * 32 + lane]);
+                    }
+                }
+            }
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                acc[e] = acc[e] * corr + w * Elem<T>::to_f(Vp[at + e * 32 + lane]);
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) x[j] += __shfl_xor_sync(0xffffffffu, x[j], d);
+                x[j] *= scale_log2;
+                if (!on[j] || x[j] == -INFINITY) continue;  // -inf: weight 0 beside any other key
+                const float mx = fmaxf(m, x[j]);
+                const float corr = m == -INFINITY ? 0.f : fast_exp2(m - mx), w = fast_exp2(x[j] - mx);
+                m = mx;
+                l = l * corr + w;
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) acc[e] = acc[e] * corr + w * v[j][e];
+            }
+            if (l != l) {  // a score was NaN: so is the whole row
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) acc[e] = l;
+                return;
+            }
         }
     }
 }
@@ -356,5 +374,15 @@ struct ChunkArgs {
 };
 size_t chunk_scratch_bytes(const gqe_shape* s);
 cudaError_t launch_chunk(const ChunkArgs& a);
+
+// How a kernel tiles its units: query rows per tile, tiles per unit, keys per
+// step, a unit's fixed cost and the smallest part in keys, blocks per SM.
+struct ChunkTiling {
+    int rows, tiles, keys, unit_keys, min_cost, per_sm;
+};
+ChunkTiling chunk_simt_tiling();
+cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a, int parts);
+ChunkTiling chunk_tc_tiling();
+cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a, int parts);
 
 }  // namespace gqe

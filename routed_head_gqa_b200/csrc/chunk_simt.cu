@@ -1,6 +1,6 @@
 // chunk_simt.cu -- routed attention of ragged chunks of new tokens over a paged
-// cache on the CUDA cores (every type and head width), and the merge of the
-// partial units.  See chunk.cuh for the units and the schedule.
+// cache on the CUDA cores (every type and head width).  See chunk.cuh for the
+// units and the schedule.
 //
 // Per unit: up to 64 query rows, 64 keys a step, one pass over the keys with the
 // running row maximum and sum (S = Q K^T, P = 2^(S c - m), O += P V, rescaled
@@ -310,149 +310,27 @@ chunk_simt_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restric
     cp_async_wait<0>();
 }
 
-// Merge of a split unit: O = gate * sum_p 2^(lse_p - M) o_p / sum_p 2^(lse_p - M)
-// over its parts in order (reproducible).  Block (c, y) takes the unit whose
-// first steps part c holds (its slot 2c + 1), one warp per row, rows y apart.
-constexpr int kCombineWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kCombineWarps)
-chunk_combine_kernel(const ChunkGeom u, int parts, T* __restrict__ O) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int kRec = D + 4, kPer = D / 32;
-    __shared__ int16_t list[kChunkMaxParts];  // the unit's slots in order
-    __shared__ int count;
-    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const ChunkDesc d = u.desc[2 * c + 1];
-    if (!d.valid || d.s1 == d.steps) return;
-    if (warp == 0) {
-        int n = 1;
-        if (lane == 0) list[0] = (int16_t)(2 * c + 1);
-        for (int p0 = c + 1; p0 < parts; p0 += 32) {
-            const int p = p0 + lane;
-            bool mine = false, other = false;
-            if (p < parts) {
-                const ChunkDesc e = u.desc[2 * p];
-                mine = e.valid && e.q == d.q && e.t0 == d.t0 && e.b == d.b;
-                other = e.valid && !mine;
-            }
-            const unsigned in = __ballot_sync(0xffffffffu, mine), out = __ballot_sync(0xffffffffu, other);
-            if (mine) list[n + __popc(in & ((1u << lane) - 1u))] = (int16_t)(2 * p);
-            n += __popc(in);
-            if (out) break;  // a later unit's part: this unit's are all behind
-        }
-        if (lane == 0) count = n;
-    }
-    __syncthreads();
-    const int n = count, rows = d.nt * u.k;
-    for (int r = blockIdx.y * kCombineWarps + warp; r < rows; r += gridDim.y * kCombineWarps) {
-        const int token = d.t0 + r / u.k, slot = r % u.k;
-        const int j = u.idx[((int64_t)token * u.g + d.q) * u.k + slot];
-        if (j < d.q * u.hpg || j >= (d.q + 1) * u.hpg) continue;
-        float M = -INFINITY;
-        bool nan = false;
-        for (int i = lane; i < n; i += 32) {
-            const float x = u.part[((int64_t)list[i] * u.row_cap + r) * kRec + D];
-            M = fmaxf(M, x);
-            nan |= x != x;
-        }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        if (__any_sync(0xffffffffu, nan)) M = NAN;
-        float L = 0.f, acc[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float* rec = u.part + ((int64_t)list[i] * u.row_cap + r) * kRec;
-            const float lse = rec[D];
-            if (lse == -INFINITY) continue;  // this part holds no key of the row
-            const float w = fast_exp2(lse - M);
-            L += w;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(rec[e * 32 + lane], w, acc[e]);
-        }
-        const float f = u.gate[((int64_t)token * u.g + d.q) * u.k + slot] / L;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            O[((int64_t)token * u.h + j) * D + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
-    }
-}
-
-int device_sms() {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
-    return sms;
-}
-
-size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
-
-int simt_parts() {
-    const int p = 2 * device_sms();
-    return p < kChunkMaxParts ? p : kChunkMaxParts;
-}
-
-ChunkGeom make_geom(const ChunkArgs& a, int bm, int bn, int parts) {
-    const gqe_shape& s = *a.s;
-    ChunkGeom u;
-    u.T = s.T;
-    u.n_seqs = a.n_seqs;
-    u.h = s.h;
-    u.g = s.g;
-    u.k = s.k;
-    u.hpg = s.h / s.g;
-    u.WU = bm / s.k;
-    u.BN = bn;
-    u.unit_keys = 2 * bn;
-    u.min_cost = 4 * bn;
-    u.row_cap = (int64_t)s.T * s.k < bm ? s.T * s.k : bm;
-    u.cap = a.max_blocks << a.page_shift;
-    u.window = a.window >= u.cap ? 0 : a.window;
-    u.sinks = u.window ? a.sinks : 0;
-    u.page_shift = a.page_shift;
-    u.num_pages = a.num_pages;
-    u.max_blocks = a.max_blocks;
-    u.cu = a.cu_new;
-    u.lengths = a.lengths;
-    u.block_table = a.block_table;
-    u.idx = a.idx;
-    u.gate = a.gate;
-    u.status = a.status;
-    u.desc = static_cast<ChunkDesc*>(a.scratch);
-    u.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) + a256(2 * parts * sizeof(ChunkDesc)));
-    return u;
-}
-
-template <typename T, int D>
-cudaError_t launch_simt(const ChunkArgs& a) {
-    const int parts = simt_parts();
-    const ChunkGeom u = make_geom(a, kBM, kBN, parts);
+cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a, int parts) {
     const size_t smem = SimtCfg<T, D>::kSmem;
     cudaError_t err = cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
     chunk_simt_kernel<T, D><<<parts, kThreads, smem, a.stream>>>(u, (const T*)a.Q, (const T*)a.K_pages,
                                                                  (const T*)a.V_pages, (T*)a.O, scale_log2);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    chunk_combine_kernel<T, D><<<dim3(parts, 2), 32 * kCombineWarps, 0, a.stream>>>(u, parts, (T*)a.O);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t chunk_scratch_bytes(const gqe_shape* s) {
-    const int64_t rows = (int64_t)s->T * s->k < kBM ? (int64_t)s->T * s->k : kBM;
-    const size_t parts = (size_t)simt_parts();
-    return a256(2 * parts * sizeof(ChunkDesc)) + a256(2 * parts * rows * (s->d_h + 4) * sizeof(float));
-}
+ChunkTiling chunk_simt_tiling() { return {kBM, 1, kBN, 2 * kBN, 4 * kBN, 2}; }
 
-cudaError_t launch_chunk(const ChunkArgs& a) {
+cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a, int parts) {
     const bool bf = a.s->dtype == GQE_BF16;
     switch (a.s->d_h) {
-        case 32: return bf ? launch_simt<__nv_bfloat16, 32>(a) : launch_simt<float, 32>(a);
-        case 64: return bf ? launch_simt<__nv_bfloat16, 64>(a) : launch_simt<float, 64>(a);
-        case 128: return bf ? launch_simt<__nv_bfloat16, 128>(a) : launch_simt<float, 128>(a);
+        case 32: return bf ? launch_typed<__nv_bfloat16, 32>(u, a, parts) : launch_typed<float, 32>(u, a, parts);
+        case 64: return bf ? launch_typed<__nv_bfloat16, 64>(u, a, parts) : launch_typed<float, 64>(u, a, parts);
+        case 128: return bf ? launch_typed<__nv_bfloat16, 128>(u, a, parts) : launch_typed<float, 128>(u, a, parts);
         default: return cudaErrorInvalidValue;
     }
 }
