@@ -5,60 +5,92 @@
 namespace gqe {
 namespace {
 
-// Merge of a split unit: O = gate * sum_p 2^(lse_p - M) o_p / sum_p 2^(lse_p - M)
-// over its parts in order (reproducible).  Block (c, y) takes the unit whose
-// first steps part c holds (its slot 2c + 1), one warp per row, rows y apart.
+// After the tile kernel: block (c, y) of a kind
+//  1. takes again the rows of CTA c's whole units whose result is not finite
+//     (only if the CTA has flagged one): see chunk_row;
+//  2. merges the split unit whose first steps part c holds as its last:
+//     O = gate * sum_p 2^(lse_p - M) o_p / sum_p 2^(lse_p - M) over its parts in
+//     order (reproducible), one warp per row, rows y apart.
 constexpr int kCombineWarps = 8;
+
+// A unit's row from the formula into O.
+template <typename T, int D>
+__device__ __noinline__ void row_again(const ChunkGeom& u, const ChunkItem& it, int r, int head, const T* Q, const T* Kp,
+                                       const T* Vp, float scale_log2, T* O) {
+    const int lane = threadIdx.x & 31, token = it.t0 + r / u.k;
+    const int64_t row = ((int64_t)token * u.h + head) * D;
+    float acc[D / 32], m, l;
+    chunk_row<T, D>(u, it, it.p0 + r / u.k, Q + row, Kp, Vp, scale_log2, acc, m, l);
+    const float f = u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] / l;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) O[row + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kCombineWarps)
-chunk_combine_kernel(const ChunkGeom u, int parts, T* __restrict__ O) {
+chunk_combine_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
+                     float scale_log2, T* __restrict__ O) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kRec = D + 4, kPer = D / 32;
-    __shared__ int16_t list[kChunkMaxParts];  // the unit's slots in order
+    __shared__ int list[kChunkMaxParts];  // the unit's records in order
     __shared__ int count;
-    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ ChunkSplit split;
+    const int c = blockIdx.x, kind = c < u.parts ? 0 : 1, cta = c - kind * u.parts, end = (kind + 1) * u.parts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ChunkDesc d = u.desc[2 * c + 1];
-    if (!d.valid || d.s1 == d.steps) return;
+    const bool odd = u.odd[c] != 0;
     if (warp == 0) {
         int n = 1;
-        if (lane == 0) list[0] = (int16_t)(2 * c + 1);
-        for (int p0 = c + 1; p0 < parts; p0 += 32) {
+        if (lane == 0) list[0] = d.rec;
+        for (int p0 = c + 1; p0 < end; p0 += 32) {
             const int p = p0 + lane;
-            bool mine = false, other = false;
-            if (p < parts) {
-                const ChunkDesc e = u.desc[2 * p];
+            bool mine = false, other = p >= end;
+            ChunkDesc e;
+            if (p < end) {
+                e = u.desc[2 * p];  // in flight with d
                 mine = e.valid && e.q == d.q && e.t0 == d.t0 && e.b == d.b;
                 other = e.valid && !mine;
             }
             const unsigned in = __ballot_sync(0xffffffffu, mine), out = __ballot_sync(0xffffffffu, other);
-            if (mine) list[n + __popc(in & ((1u << lane) - 1u))] = (int16_t)(2 * p);
+            if (mine) list[n + __popc(in & ((1u << lane) - 1u))] = e.rec;
             n += __popc(in);
-            if (out) break;  // a later unit's part: this unit's are all behind
+            if (out || !d.valid) break;  // a later unit's part: this unit's are all behind
         }
         if (lane == 0) count = n;
     }
+    if (odd) {
+        chunk_split(u, split, cta);
+        ChunkWalk walk(u, split, kind, cta);
+        ChunkItem it;
+        while (walk.next(u, it, false)) {
+            if (it.rec >= 0) continue;
+            for (int r = blockIdx.y * kCombineWarps + warp; r < it.nt * u.k; r += gridDim.y * kCombineWarps) {
+                const int token = it.t0 + r / u.k, j = u.idx[((int64_t)token * u.g + it.q) * u.k + r % u.k];
+                if (j < it.q * u.hpg || j >= (it.q + 1) * u.hpg) continue;
+                float check = 0.f;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) check += 0.f * Elem<T>::to_f(O[((int64_t)token * u.h + j) * D + e * 32 + lane]);
+                if (__any_sync(0xffffffffu, !(check == 0.f))) row_again<T, D>(u, it, r, j, Q, Kp, Vp, scale_log2, O);
+            }
+        }
+    }
+    if (!d.valid) return;
     __syncthreads();
     const int n = count, rows = d.nt * u.k;
     for (int r = blockIdx.y * kCombineWarps + warp; r < rows; r += gridDim.y * kCombineWarps) {
         const int token = d.t0 + r / u.k, slot = r % u.k;
         const int j = u.idx[((int64_t)token * u.g + d.q) * u.k + slot];
-        if (j < d.q * u.hpg || j >= (d.q + 1) * u.hpg) continue;
+        const float gate = u.gate[((int64_t)token * u.g + d.q) * u.k + slot];
         float M = -INFINITY;
-        bool nan = false;
-        for (int i = lane; i < n; i += 32) {
-            const float x = u.part[((int64_t)list[i] * u.row_cap + r) * kRec + D];
-            M = fmaxf(M, x);
-            nan |= x != x;
-        }
+        for (int i = lane; i < n; i += 32) M = fmaxf(M, u.part[(int64_t)(list[i] + r) * kRec + D]);
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        if (__any_sync(0xffffffffu, nan)) M = NAN;
         float L = 0.f, acc[kPer];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
-            const float* rec = u.part + ((int64_t)list[i] * u.row_cap + r) * kRec;
+            const float* rec = u.part + (int64_t)(list[i] + r) * kRec;
             const float lse = rec[D];
             if (lse == -INFINITY) continue;  // this part holds no key of the row
             const float w = fast_exp2(lse - M);
@@ -66,7 +98,18 @@ chunk_combine_kernel(const ChunkGeom u, int parts, T* __restrict__ O) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e) acc[e] = fmaf(rec[e * 32 + lane], w, acc[e]);
         }
-        const float f = u.gate[((int64_t)token * u.g + d.q) * u.k + slot] / L;
+        if (j < d.q * u.hpg || j >= (d.q + 1) * u.hpg) continue;  // no such row: its records hold nothing
+        float check = L * 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) check += acc[e] * 0.f;
+        if (__any_sync(0xffffffffu, !(check == 0.f))) {
+            const ChunkSeq s = chunk_seq(u, d.b);
+            ChunkItem it;
+            chunk_item(u, s, d.b, d.q, (d.t0 - s.t0) / u.WU, it);
+            row_again<T, D>(u, it, r, j, Q, Kp, Vp, scale_log2, O);
+            continue;
+        }
+        const float f = gate / L;
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
             O[((int64_t)token * u.h + j) * D + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
@@ -97,6 +140,13 @@ int row_cap(const gqe_shape* s, const ChunkTiling& t) {
     return (int)(all < unit ? all : unit);
 }
 
+int few_cap(const gqe_shape* s, const ChunkTiling& t) {
+    return (int64_t)s->T * s->k < t.few ? s->T * s->k : t.few;
+}
+
+size_t desc_bytes(int parts) { return a256(4 * (size_t)parts * sizeof(ChunkDesc)); }
+size_t odd_bytes(int parts) { return a256(2 * (size_t)parts * sizeof(int32_t)); }
+
 ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     const gqe_shape& s = *a.s;
     ChunkGeom u;
@@ -109,12 +159,17 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     u.W = t.rows / s.k;
     u.WU = t.tiles * u.W;
     u.BN = t.keys;
+    u.bn_shift = 0;
+    while ((1 << u.bn_shift) < t.keys) ++u.bn_shift;
     u.unit_keys = t.unit_keys;
-    u.min_cost = t.min_cost;
+    u.per_min = 1.0f / t.min_cost;
+    u.few = t.few;
+    u.parts = parts;
     u.row_cap = row_cap(&s, t);
+    u.few_cap = few_cap(&s, t);
     u.cap = a.max_blocks << a.page_shift;
     u.window = a.window >= u.cap ? 0 : a.window;
-    u.sinks = u.window ? a.sinks : 0;
+    u.sinks = u.window == 0 ? 0 : a.sinks < u.cap ? a.sinks : u.cap;
     u.page_shift = a.page_shift;
     u.num_pages = a.num_pages;
     u.max_blocks = a.max_blocks;
@@ -125,14 +180,15 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     u.gate = a.gate;
     u.status = a.status;
     u.desc = static_cast<ChunkDesc*>(a.scratch);
-    u.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) + a256(2 * (size_t)parts * sizeof(ChunkDesc)));
+    u.odd = reinterpret_cast<int32_t*>(static_cast<char*>(a.scratch) + desc_bytes(parts));
+    u.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) + desc_bytes(parts) + odd_bytes(parts));
     return u;
 }
 
 template <typename T>
-cudaError_t launch_combine(const ChunkGeom& u, const ChunkArgs& a, int parts, int blocks) {
+cudaError_t launch_combine(const ChunkGeom& u, const ChunkArgs& a, int kinds, int blocks) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(parts, blocks);
+    cfg.gridDim = dim3(kinds * u.parts, blocks);
     cfg.blockDim = dim3(32 * kCombineWarps);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
@@ -140,10 +196,14 @@ cudaError_t launch_combine(const ChunkGeom& u, const ChunkArgs& a, int parts, in
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    auto go = [&](auto kernel) {
+        return cudaLaunchKernelEx(&cfg, kernel, u, (const T*)a.Q, (const T*)a.K_pages, (const T*)a.V_pages,
+                                  1.4426950408889634f / sqrtf((float)a.s->d_h), (T*)a.O);
+    };
     switch (a.s->d_h) {
-        case 32: return cudaLaunchKernelEx(&cfg, chunk_combine_kernel<T, 32>, u, parts, (T*)a.O);
-        case 64: return cudaLaunchKernelEx(&cfg, chunk_combine_kernel<T, 64>, u, parts, (T*)a.O);
-        default: return cudaLaunchKernelEx(&cfg, chunk_combine_kernel<T, 128>, u, parts, (T*)a.O);
+        case 32: return go(chunk_combine_kernel<T, 32>);
+        case 64: return go(chunk_combine_kernel<T, 64>);
+        default: return go(chunk_combine_kernel<T, 128>);
     }
 }
 
@@ -151,19 +211,20 @@ cudaError_t launch_combine(const ChunkGeom& u, const ChunkArgs& a, int parts, in
 
 size_t chunk_scratch_bytes(const gqe_shape* s) {
     const ChunkTiling t = tiling(s);
-    const size_t parts = (size_t)max_parts(t);
-    return a256(2 * parts * sizeof(ChunkDesc)) + a256(2 * parts * row_cap(s, t) * (size_t)(s->d_h + 4) * sizeof(float));
+    const size_t parts = (size_t)max_parts(t), rows = 2 * parts * (row_cap(s, t) + few_cap(s, t));
+    return desc_bytes((int)parts) + odd_bytes((int)parts) + a256(rows * (size_t)(s->d_h + 4) * sizeof(float));
 }
 
 cudaError_t launch_chunk(const ChunkArgs& a) {
     const ChunkTiling t = tiling(a.s);
     const int parts = max_parts(t);
     const ChunkGeom u = make_geom(a, t, parts);
-    const cudaError_t err = on_tensor_cores(a.s) ? launch_chunk_tc(u, a, parts) : launch_chunk_simt(u, a, parts);
+    const cudaError_t err = on_tensor_cores(a.s) ? launch_chunk_tc(u, a) : launch_chunk_simt(u, a);
     if (err != cudaSuccess) return err;
     const int blocks = (u.row_cap + 4 * kCombineWarps - 1) / (4 * kCombineWarps);  // about four rows a warp
-    return a.s->dtype == GQE_BF16 ? launch_combine<__nv_bfloat16>(u, a, parts, blocks)
-                                  : launch_combine<float>(u, a, parts, blocks);
+    const int kinds = t.few > 0 ? 2 : 1;
+    return a.s->dtype == GQE_BF16 ? launch_combine<__nv_bfloat16>(u, a, kinds, blocks)
+                                  : launch_combine<float>(u, a, kinds, blocks);
 }
 
 }  // namespace gqe

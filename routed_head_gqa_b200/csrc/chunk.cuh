@@ -21,6 +21,8 @@
 // chunk_combine_kernel merges in order.  So one long cache, many short ones and
 // a mix of decodes and prompt chunks all spread evenly, and a part holds at
 // most two partial units: its first (slot 2c) and its last (slot 2c + 1).
+// Requests of few query rows (u.few) are split by themselves, so that a kernel
+// can treat them in another way: two kinds of units, each over all CTAs.
 #pragma once
 
 #include "common.cuh"
@@ -32,16 +34,18 @@ constexpr uint32_t kWhereChunk = 8;        // status "where" id of the chunk ker
 
 // One partial unit: what the merge needs to find its rows.
 struct ChunkDesc {
-    int32_t valid, b, q, t0, nt, s0, s1, steps;
+    int32_t valid, b, q, t0, nt, rec;
 };
 
 struct ChunkGeom {
     int T, n_seqs, h, g, k, hpg;
     int W, WU;        // tokens per query tile and per unit
-    int BN;           // keys per step
+    int BN, bn_shift; // keys per step and their log2
     int unit_keys;    // a unit's fixed cost, in keys
-    int min_cost;     // smallest cost worth a part, in keys
-    int row_cap;      // query rows a partial record set holds
+    float per_min;    // 1 / the smallest cost worth a part, in keys
+    int few;          // query rows up to which a request is of the second kind
+    int parts;        // CTAs, and parts of either kind at most
+    int row_cap, few_cap;  // query rows that the partial records of a unit take, by kind
     int window, sinks;
     int cap;          // rows a block table can hold: page_size * max_blocks
     int page_shift, num_pages, max_blocks;
@@ -51,8 +55,9 @@ struct ChunkGeom {
     const int32_t* idx;
     const float* gate;
     void* status;
-    ChunkDesc* desc;  // [2 * parts]
-    float* part;      // [2 * parts][row_cap][D + 4]
+    ChunkDesc* desc;  // [2 kinds][parts][2]
+    int32_t* odd;     // [2 kinds][CTAs]: a result of the CTA's whole units is not finite
+    float* part;      // [2 * parts * row_cap + 2 * parts * few_cap][D + 4]
 };
 
 struct ChunkItem {
@@ -63,6 +68,7 @@ struct ChunkItem {
     int lo_tile;           // steps sink_tiles .. are tiles lo_tile ..
     int lo, hi;            // keys [lo, hi) and, below lo, keys < sinks are seen by some row
     int steps, s0, s1;     // the unit's steps and this part's [s0, s1)
+    int rec;               // the unit's first partial record if it is split, else -1
     __device__ __forceinline__ int tile(int s) const { return s < sink_tiles ? s : lo_tile + (s - sink_tiles); }
 };
 
@@ -92,19 +98,26 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkGeom& u, int b) {
     return s;
 }
 
+// 0: many query rows, 1: few.
+__device__ __forceinline__ int chunk_kind(const ChunkGeom& u, int n) { return n <= u.few / u.k ? 1 : 0; }
+
 __device__ __forceinline__ int chunk_units(const ChunkGeom& u, int n) { return (n + u.WU - 1) / u.WU; }
 
 // Cost of the first i units of a request and group, in keys, in closed form:
 // unit j sees about first + j * WU keys, or the window's span if that is less.
-__device__ __forceinline__ int64_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s, int64_t i) {
-    const int64_t first = (int64_t)s.L - s.n + min(s.n, u.WU);
-    const int64_t span = u.window ? (int64_t)u.window + u.WU + u.sinks : (int64_t)1 << 40;
-    int64_t grow = 0;
-    if (first < span) {
-        grow = (span - first + u.WU - 1) / u.WU;
-        if (grow > i) grow = i;
+__device__ __forceinline__ int64_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s, int i) {
+    const int first = s.L - s.n + min(s.n, u.WU);
+    int64_t cost = (int64_t)i * u.unit_keys;
+    int grow = i;
+    if (u.window) {
+        const int64_t span = (int64_t)u.window + u.WU + u.sinks;  // below 2^32: window and sinks are at most 2^30
+        grow = first < span ? min((uint32_t)i, ((uint32_t)(span - first) + u.WU - 1) / (uint32_t)u.WU) : 0;
+        cost += (i - grow) * span;
     }
-    return grow * first + u.WU * (grow * (grow - 1) / 2) + (i - grow) * span + i * u.unit_keys;
+    return cost + (int64_t)grow * first + u.WU * ((int64_t)grow * (grow - 1) / 2);
+}
+__device__ __forceinline__ int64_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s) {
+    return s.n > 0 ? u.g * chunk_cost(u, s, chunk_units(u, s.n)) : 0;
 }
 
 __device__ __forceinline__ void chunk_item(const ChunkGeom& u, const ChunkSeq& s, int b, int q, int i, ChunkItem& it) {
@@ -116,9 +129,9 @@ __device__ __forceinline__ void chunk_item(const ChunkGeom& u, const ChunkSeq& s
     it.p0 = s.L - s.n + first;
     it.hi = it.p0 + it.nt;
     it.lo = u.window ? max(0, it.p0 - u.window + 1) : 0;
-    it.lo_tile = it.lo / u.BN;
-    it.sink_tiles = min(it.lo_tile, (min(u.sinks, it.lo) + u.BN - 1) / u.BN);
-    it.steps = it.sink_tiles + (it.hi + u.BN - 1) / u.BN - it.lo_tile;
+    it.lo_tile = it.lo >> u.bn_shift;
+    it.sink_tiles = min(it.lo_tile, (min(u.sinks, it.lo) + u.BN - 1) >> u.bn_shift);
+    it.steps = it.sink_tiles + ((it.hi + u.BN - 1) >> u.bn_shift) - it.lo_tile;
 }
 
 // Whether a row at position p sees key s.
@@ -131,14 +144,17 @@ struct ChunkPlace {
     int b, q, i, s;
 };
 
-// Where a cost `rest` (within request b's own cost) falls.
-__device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, int b, int64_t rest) {
-    const ChunkSeq s = chunk_seq(u, b);
+// Where a cost `rest` (within request b's own cost) falls.  The quotients are
+// taken in fp32: they only place the boundaries, and the two parts that meet at
+// one evaluate the same expression.
+__device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const ChunkSeq& s, int b, int64_t rest) {
     const int units = chunk_units(u, s.n);
     const int64_t per = chunk_cost(u, s, units);
     ChunkPlace pl;
     pl.b = b;
-    pl.q = (int)(rest / per);
+    pl.q = min((int)__fdividef((float)rest, (float)per), u.g - 1);
+    if (pl.q > 0 && rest < pl.q * per) --pl.q;
+    if (pl.q + 1 < u.g && rest >= (pl.q + 1) * per) ++pl.q;
     rest -= pl.q * per;
     int lo = 0, hi = units - 1;  // the last unit whose prefix does not exceed rest
     while (lo < hi) {
@@ -149,61 +165,74 @@ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, int b, int
     const int64_t before = chunk_cost(u, s, lo), cost = chunk_cost(u, s, lo + 1) - before;
     ChunkItem it;
     chunk_item(u, s, b, pl.q, lo, it);
-    pl.s = (int)((rest - before) * it.steps / cost);
+    pl.s = max(0, min((int)(__fdividef((float)(rest - before), (float)cost) * it.steps), it.steps - 1));
     return pl;
 }
 
 // Shared state of the split: filled by chunk_split, read by the item walk.
 struct ChunkSplit {
-    int64_t warp_sum[32];
-    ChunkPlace from, to;
-    int parts;
+    int64_t warp_sum[2][32];
+    ChunkPlace from[2], to[2];  // by kind
 };
 
-// This part's first place and the first place that is no longer its own.
-// Called by all threads of the block (blockDim.x a multiple of 32, at most 1024).
-__device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, int c, int max_parts) {
+// The part that a CTA takes of a kind: opposite ends, so that small amounts of
+// both go to different CTAs.
+__device__ __forceinline__ int chunk_part(const ChunkGeom& u, int kind, int cta) { return kind ? cta : u.parts - 1 - cta; }
+
+// A CTA's first place and the first place that is no longer its own, of each
+// kind.  Called by all threads of a block (at most 1024, whole warps).
+__device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, int cta) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
     const int per = (u.n_seqs + blockDim.x - 1) / blockDim.x;
     const int b0 = min(tid * per, u.n_seqs), b1 = min(b0 + per, u.n_seqs);
-    int64_t mine = 0;
+    ChunkSeq only;  // the request of a thread that has one
+    int64_t mine[2] = {0, 0};
     for (int b = b0; b < b1; ++b) {
-        const ChunkSeq s = chunk_seq(u, b);
-        if (s.n > 0) mine += u.g * chunk_cost(u, s, chunk_units(u, s.n));
+        only = chunk_seq(u, b);
+        const int64_t cost = chunk_cost(u, only);
+        if (chunk_kind(u, only.n)) mine[1] += cost; else mine[0] += cost;
     }
-    int64_t run = mine;
+    if (tid < 2) {  // overwritten below where the place exists
+        sp.from[tid] = {u.n_seqs, 0, 0, 0};
+        sp.to[tid] = {u.n_seqs, 0, 0, 0};
+    }
+    int64_t run[2];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, run, d);
-        if (lane >= d) run += o;
-    }
-    if (lane == 31) sp.warp_sum[warp] = run;
-    if (tid == 0) {  // overwritten below where the place exists
-        sp.from = {u.n_seqs, 0, 0, 0};
-        sp.to = {u.n_seqs, 0, 0, 0};
+    for (int kind = 0; kind < 2; ++kind) {
+        run[kind] = mine[kind];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, run[kind], d);
+            if (lane >= d) run[kind] += o;
+        }
+        if (lane == 31) sp.warp_sum[kind][warp] = run[kind];
     }
     __syncthreads();
-    int64_t before = run - mine, total = 0;
-    for (int w = 0; w < nw; ++w) {
-        if (w < warp) before += sp.warp_sum[w];
-        total += sp.warp_sum[w];
-    }
-    int64_t want = total / u.min_cost;
-    const int parts = (int)(want < 1 ? 1 : want > max_parts ? max_parts : want);
-    if (tid == 0) sp.parts = parts;
-    if (c < parts && total > 0) {
-        const int64_t each = total / parts, left = total % parts;
-        const int64_t x0 = c * each + c * left / parts, x1 = (c + 1) * each + (c + 1) * left / parts;
-#pragma unroll
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const int64_t own = kind ? mine[1] : mine[0];
+        int64_t before = (kind ? run[1] : run[0]) - own, total = 0;
+        for (int w = 0; w < nw; ++w) {
+            if (w < warp) before += sp.warp_sum[kind][w];
+            total += sp.warp_sum[kind][w];
+        }
+        const float want = (float)total * u.per_min;
+        const int parts = want < 1.f ? 1 : want > (float)u.parts ? u.parts : (int)want;
+        const int c = chunk_part(u, kind, cta);
+        if (c >= parts || own == 0) continue;
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-            const int64_t x = e ? x1 : x0;
-            if (x < before || x >= before + mine) continue;
+            if (c + e == parts) break;  // the last part ends with the step
+            const uint32_t frac = (uint32_t)(__fdiv_rn((float)(c + e), (float)parts) * 4294967296.f);
+            const int64_t x = (total >> 32) * frac + (int64_t)(((uint64_t)(uint32_t)total * frac) >> 32);  // total * (c + e) / parts
+            if (x < before || x >= before + own) continue;
             int64_t at = before;
             for (int b = b0; b < b1; ++b) {
-                const ChunkSeq s = chunk_seq(u, b);
-                const int64_t cost = s.n > 0 ? u.g * chunk_cost(u, s, chunk_units(u, s.n)) : 0;
+                const ChunkSeq s = per == 1 ? only : chunk_seq(u, b);
+                const int64_t cost = chunk_kind(u, s.n) == kind ? chunk_cost(u, s) : 0;
                 if (x < at + cost) {
-                    (e ? sp.to : sp.from) = chunk_place(u, b, x - at);
+                    const ChunkPlace pl = chunk_place(u, s, b, x - at);
+                    if (e) sp.to[kind] = pl; else sp.from[kind] = pl;
                     break;
                 }
                 at += cost;
@@ -213,26 +242,34 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
     __syncthreads();
 }
 
-// Walks a part's items in order.
+// Walks a CTA's items of a kind in order.  Warp-collective: the lanes hold 32
+// requests, so that a run of short ones costs one round of loads.
 struct ChunkWalk {
     ChunkPlace at, to;
-    ChunkSeq seq;
-    int units, loaded;
-    __device__ __forceinline__ explicit ChunkWalk(const ChunkSplit& sp) : at(sp.from), to(sp.to), units(0), loaded(-1) {}
-    __device__ __forceinline__ bool next(const ChunkGeom& u, ChunkItem& it) {
+    ChunkSeq held;       // request base + lane
+    int kind, base, part;
+    __device__ __forceinline__ ChunkWalk(const ChunkGeom& u, const ChunkSplit& sp, int kind, int cta)
+        : at(sp.from[kind]), to(sp.to[kind]), kind(kind), base(-64), part(chunk_part(u, kind, cta)) {}
+    // describe: write the descriptors of split units
+    __device__ __forceinline__ bool next(const ChunkGeom& u, ChunkItem& it, bool describe = true) {
+        const int lane = threadIdx.x & 31;
         while (true) {
             if (at.b >= u.n_seqs || at.b > to.b) return false;
-            if (loaded != at.b) {
-                seq = chunk_seq(u, at.b);
-                units = chunk_units(u, seq.n);
-                loaded = at.b;
+            if (at.b < base || at.b >= base + 32) {
+                base = at.b;
+                held = {0, 0, 0};
+                if (base + lane < u.n_seqs) held = chunk_seq(u, base + lane);
+                if (chunk_kind(u, held.n) != kind) held.n = 0;
             }
-            if (at.i >= units) {
+            const int src = at.b - base;
+            const ChunkSeq seq = {__shfl_sync(0xffffffffu, held.t0, src), __shfl_sync(0xffffffffu, held.n, src),
+                                  __shfl_sync(0xffffffffu, held.L, src)};
+            const int units = chunk_units(u, seq.n);
+            if (at.i >= units && ++at.q < u.g && units > 0) {
                 at.i = 0;
-                if (units == 0 || ++at.q >= u.g) {
-                    at.q = 0;
-                    ++at.b;
-                }
+            } else if (at.i >= units) {  // the next request that has work of this kind, if it is among the held
+                const unsigned some = __ballot_sync(0xffffffffu, held.n > 0) & ~(src == 31 ? 0xffffffffu : (2u << src) - 1u);
+                at = {some ? base + __ffs(some) - 1 : base + 32, 0, 0, 0};
                 continue;
             }
             const bool last = at.b == to.b && at.q == to.q && at.i == to.i;
@@ -241,6 +278,12 @@ struct ChunkWalk {
             chunk_item(u, seq, at.b, at.q, at.i, it);
             it.s0 = at.s;
             it.s1 = last ? min(to.s, it.steps) : it.steps;
+            it.rec = -1;
+            if (it.s0 > 0 || it.s1 < it.steps) {
+                const int slot = it.s0 > 0 ? 2 * part : 2 * part + 1;
+                it.rec = kind ? 2 * u.parts * u.row_cap + slot * u.few_cap : slot * u.row_cap;
+                if (lane == 0 && describe) u.desc[kind * 2 * u.parts + slot] = {1, it.b, it.q, it.t0, it.nt, it.rec};
+            }
             ++at.i;
             at.s = 0;
             return true;
@@ -248,10 +291,13 @@ struct ChunkWalk {
     }
 };
 
-__device__ __forceinline__ bool chunk_partial(const ChunkItem& it) { return it.s0 > 0 || it.s1 < it.steps; }
-__device__ __forceinline__ int chunk_slot(const ChunkItem& it, int c) { return it.s0 > 0 ? 2 * c : 2 * c + 1; }
-__device__ __forceinline__ void chunk_describe(const ChunkGeom& u, const ChunkItem& it, int c) {
-    u.desc[chunk_slot(it, c)] = {1, it.b, it.q, it.t0, it.nt, it.s0, it.s1, it.steps};
+// Marks this CTA's descriptors and flags unused, before its walks (by the lane 0
+// that writes the descriptors).
+__device__ __forceinline__ void chunk_clear(const ChunkGeom& u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        u.desc[(i >> 1) * 2 * u.parts + 2 * chunk_part(u, i >> 1, blockIdx.x) + (i & 1)].valid = 0;
+    u.odd[blockIdx.x] = u.odd[u.parts + blockIdx.x] = 0;
 }
 
 // Cache row of request b's key s.  A block-table entry outside the page pool is
@@ -275,14 +321,15 @@ __device__ __forceinline__ int chunk_head(const ChunkGeom& u, int token, int q, 
     return j;
 }
 
-// One row of an item by the formula alone, key by key over the keys the row
-// sees (warp-collective; lane holds elements e * 32 + lane).  The tile kernels
-// multiply a masked key's weight 0 with its V row, so an infinity or NaN there
-// reaches rows that do not see the key; a row whose result is not finite is
-// therefore taken again here, where a key that the row does not see is not read.
+// One row of a unit by the formula alone, key by key over the keys the row sees
+// (warp-collective; lane holds elements e * 32 + lane).  The tile kernels multiply
+// a masked key's weight 0 with its V row, so an infinity or NaN there reaches rows
+// that do not see the key; a row whose result is not finite is therefore taken
+// again here (by the merge kernel: in the tile kernels the code alone would cost
+// their loops registers), where a key that the row does not see is not read.
 template <typename T, int D>
 __device__ __forceinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& it, int p, const T* q_row, const T* Kp,
-                                       const T* Vp, float scale_log2, float (&acc)[D / 32], float& m, float& l) {
+                                          const T* Vp, float scale_log2, float (&acc)[D / 32], float& m, float& l) {
     const int lane = threadIdx.x & 31;
     float qv[D / 32];
 #pragma unroll
@@ -292,9 +339,8 @@ __device__ __forceinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& i
     }
     m = -INFINITY;
     l = 0.f;
-    for (int st = it.s0; st < it.s1; ++st) {
-        const int k0 = it.tile(st) * u.BN;
-        const int k1 = min(k0 + u.BN, p + 1);
+    for (int st = 0; st < it.steps; ++st) {
+        const int k0 = it.tile(st) * u.BN, k1 = min(k0 + u.BN, p + 1);
         for (int s = k0; s < k1; s += 4) {  // four keys' loads in flight
             float x[4], v[4][D / 32];
             bool on[4];
@@ -333,26 +379,6 @@ __device__ __forceinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& i
     }
 }
 
-// Where a row's result goes: the gated row of O, or the row's partial record.
-template <typename T, int D>
-__device__ __forceinline__ void chunk_store_row(const ChunkGeom& u, const ChunkItem& it, int c, int r, int token, int head,
-                                                const float (&acc)[D / 32], float m, float l, T* O) {
-    const int lane = threadIdx.x & 31;
-    if (chunk_partial(it)) {
-        float* rec = u.part + ((int64_t)chunk_slot(it, c) * u.row_cap + r) * (D + 4);
-        const bool none = m == -INFINITY && l == 0.f;
-        const float inv = none ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) rec[e * 32 + lane] = acc[e] * inv;
-        if (lane == 0) rec[D] = none ? -INFINITY : m + log2f(l);
-    } else {
-        const float f = u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] / l;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            O[((int64_t)token * u.h + head) * D + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
-    }
-}
-
 // Arguments of a call (host).
 struct ChunkArgs {
     const gqe_shape* s;
@@ -375,14 +401,15 @@ struct ChunkArgs {
 size_t chunk_scratch_bytes(const gqe_shape* s);
 cudaError_t launch_chunk(const ChunkArgs& a);
 
-// How a kernel tiles its units: query rows per tile, tiles per unit, keys per
-// step, a unit's fixed cost and the smallest part in keys, blocks per SM.
+// How a kernel tiles its units: query rows per tile, tiles per unit, the rows up
+// to which a request is of the second kind, keys per step, a unit's fixed cost and
+// the smallest part in keys, blocks per SM.
 struct ChunkTiling {
-    int rows, tiles, keys, unit_keys, min_cost, per_sm;
+    int rows, tiles, few, keys, unit_keys, min_cost, per_sm;
 };
 ChunkTiling chunk_simt_tiling();
-cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a, int parts);
+cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a);
 ChunkTiling chunk_tc_tiling();
-cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a, int parts);
+cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a);
 
 }  // namespace gqe

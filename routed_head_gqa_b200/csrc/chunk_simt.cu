@@ -226,7 +226,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
         cp_async_commit();
     }
 
-    const bool partial = chunk_partial(it);
+    const bool partial = it.rec >= 0;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         float sum = l[i];
@@ -239,12 +239,10 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
         float check = 0.f;
 #pragma unroll
         for (int e = 0; e < kCols; ++e) check += acc[i][e] * 0.f;  // 0, or NaN when a value is not finite
-        const bool bad = j >= 0 && !(check + sum * 0.f == 0.f);
-        unsigned again = __ballot_sync(0xffffffffu, bad);
-        const bool redo = (again & (0xffffu << (tid & 16))) != 0;  // a value of this half warp's row
-        if (j >= 0 && !redo) {
+        if (j >= 0 && !(check + sum * 0.f == 0.f)) u.odd[blockIdx.x] = 1;
+        if (j >= 0) {
             const int token = it.t0 + r / u.k;
-            float* rec = partial ? u.part + ((int64_t)chunk_slot(it, blockIdx.x) * u.row_cap + r) * (D + 4) : nullptr;
+            float* rec = partial ? u.part + (int64_t)(it.rec + r) * (D + 4) : nullptr;
             T* o = O + ((int64_t)token * u.h + j) * D;
             const float f = partial ? inv : u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] * inv;
 #pragma unroll
@@ -259,17 +257,6 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
                     store_cols(o + col, out);
             }
             if (partial && tx == 0) rec[D] = none ? -INFINITY : m[i] + log2f(sum);
-        }
-        if (again != 0) {
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                if (!(again & (0xffffu << (16 * half)))) continue;
-                const int rr = ((tid >> 5) * 2 + half) + 16 * i;  // the half warp's row
-                const int jj = sh.row_j[rr], token = it.t0 + rr / u.k;
-                float a2[D / 32], m2, l2;
-                chunk_row<T, D>(u, it, it.p0 + rr / u.k, Q + ((int64_t)token * u.h + jj) * D, Kp, Vp, scale_log2, a2, m2, l2);
-                chunk_store_row<T, D>(u, it, blockIdx.x, rr, token, jj, a2, m2, l2, O);
-            }
         }
     }
 }
@@ -287,13 +274,17 @@ chunk_simt_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restric
     T* Vs = Ks + kBN * C::kKV;
     const int tid = threadIdx.x;
 
-    chunk_split(u, sh.split, blockIdx.x, gridDim.x);
-    if (tid == 0) u.desc[2 * blockIdx.x].valid = u.desc[2 * blockIdx.x + 1].valid = 0;
-    ChunkWalk walk(sh.split);
+    chunk_split(u, sh.split, blockIdx.x);
+    if (tid == 0) chunk_clear(u);
+    ChunkWalk walk(u, sh.split, 0, blockIdx.x);
     while (true) {
-        if (tid == 0) {
-            sh.has = walk.next(u, sh.item);
-            if (sh.has && chunk_partial(sh.item)) chunk_describe(u, sh.item, blockIdx.x);
+        if (tid < 32) {
+            ChunkItem it;
+            const bool has = walk.next(u, it);
+            if (tid == 0) {
+                sh.has = has;
+                sh.item = it;
+            }
         }
         __syncthreads();
         if (!sh.has) break;
@@ -311,26 +302,26 @@ chunk_simt_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restric
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a, int parts) {
+cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a) {
     const size_t smem = SimtCfg<T, D>::kSmem;
     cudaError_t err = cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-    chunk_simt_kernel<T, D><<<parts, kThreads, smem, a.stream>>>(u, (const T*)a.Q, (const T*)a.K_pages,
+    chunk_simt_kernel<T, D><<<u.parts, kThreads, smem, a.stream>>>(u, (const T*)a.Q, (const T*)a.K_pages,
                                                                  (const T*)a.V_pages, (T*)a.O, scale_log2);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-ChunkTiling chunk_simt_tiling() { return {kBM, 1, kBN, 2 * kBN, 4 * kBN, 2}; }
+ChunkTiling chunk_simt_tiling() { return {kBM, 1, 0, kBN, 2 * kBN, 4 * kBN, 2}; }
 
-cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a, int parts) {
+cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a) {
     const bool bf = a.s->dtype == GQE_BF16;
     switch (a.s->d_h) {
-        case 32: return bf ? launch_typed<__nv_bfloat16, 32>(u, a, parts) : launch_typed<float, 32>(u, a, parts);
-        case 64: return bf ? launch_typed<__nv_bfloat16, 64>(u, a, parts) : launch_typed<float, 64>(u, a, parts);
-        case 128: return bf ? launch_typed<__nv_bfloat16, 128>(u, a, parts) : launch_typed<float, 128>(u, a, parts);
+        case 32: return bf ? launch_typed<__nv_bfloat16, 32>(u, a) : launch_typed<float, 32>(u, a);
+        case 64: return bf ? launch_typed<__nv_bfloat16, 64>(u, a) : launch_typed<float, 64>(u, a);
+        case 128: return bf ? launch_typed<__nv_bfloat16, 128>(u, a) : launch_typed<float, 128>(u, a);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -3,8 +3,13 @@
 // window.  See chunk.cuh for the units, the schedule and the masks.
 //
 // A unit has up to two query tiles of 128 rows (W = floor(128 / k) tokens of k
-// rows each) over one stream of 128-key K/V tiles; a decode has one tile of k
-// rows, and only the warp that holds them works on its softmax.
+// rows each) over one stream of 128-key K/V tiles.  A unit of at most 16 rows (a
+// decode, or a few tokens of it) is turned around: the keys take the 128 lanes,
+// S^T = K Q^T is 128 x 16 and O^T += V^T P 128 x 16, so that all threads share
+// the exponentials of a step (as one row per thread, k threads would work and
+// 128 - k would wait: 3500 clocks a step, 1.8 times what the step's K/V take from
+// HBM) and the MMAs shrink with the rows.  Its two warpgroups take every other
+// step, each with its own maximum, sum and O^T, merged at the end of the item.
 //
 // Roles (384 threads, one persistent CTA per SM):
 //   warp 0      K/V tiles by TMA: one box per page (of at most 128 rows) and
@@ -18,10 +23,13 @@
 //               last token, outside the window): their weight is 0, but 0 times
 //               what an unused row holds may be NaN.
 //   warps 4-7   softmax, epilogue and zero fill of query tile 0, a row per thread
-//   warps 8-11  the same for query tile 1
+//               (few rows: the even steps, a key per thread)
+//   warps 8-11  the same for query tile 1 (few rows: the odd steps)
 // TMEM: one S buffer [0,128) that the tiles take in turn, P_0 [128,192) and P_1
 // [192,256) (bf16 pairs), O_0 [256,384), O_1 [384,512).  The softmax copies S to
-// registers and hands the buffer back at once, so the next S runs under it.
+// registers and hands the buffer back at once, so the next S runs under it.  Few
+// rows: S^T_t [64 t, 64 t + 16), O^T_t the first 16 columns of O_t, P in shared
+// memory as the second operand.
 //
 // Rounding: P is rounded to bf16 for the second product (half a step, 2^-8 of
 // each weight, the same size as the output's own rounding); the row sums take
@@ -41,6 +49,7 @@ using namespace sm100;
 using bf16 = __nv_bfloat16;
 
 constexpr int kD = 128, kBM = 128, kBN = 128, kQT = 2, kThreads = 384;
+constexpr int kFew = 16;                   // query rows up to which a unit is turned around
 constexpr int kItems = 4;                  // items in flight between the walk and the other roles
 constexpr uint32_t kHalf = 128 * 64 * 2;   // one [128][64] bf16 box, 16 KB
 constexpr uint32_t kTileBytes = 2 * kHalf;
@@ -56,22 +65,25 @@ struct Smem {
     uint8_t q[kQT][kTileBytes];
     uint8_t k[2][kTileBytes];
     uint8_t v[2][kTileBytes];
+    uint8_t p[kQT][kFew * 256];          // few rows: P_t [16 rows][128 keys] bf16, two 64-key halves
+    float x[kFew][kD];                   // few rows: O^T_1 on its way to warpgroup 0
+    float x_ml[2][kFew];                 //   with its maxima and sums
+    float4 wmax[kQT][2][kFew];           // few rows: the four warps' maxima of a step
+    float4 wsum[kQT][kFew];              //   and their sums at the end
     ChunkItem item[kItems];
-    int32_t has[kItems];                 // 0: no more items
+    int32_t has[kItems];                 // 0: no more items of the kind
     int32_t row_j[kItems][kQT][kBM];     // head of each query row, -1: none
     ChunkSplit split;
     uint64_t item_full[kItems], item_free[kItems], rows_full[kItems];
     uint64_t kv_full_k[2], kv_full_v[2], kv_empty_k[2], kv_empty_v[2];
     uint64_t s_full[kQT], p_full[kQT], p_empty[kQT], o_full[kQT], o_empty[kQT];
+    uint64_t st_free[kQT], vote[kQT], x_full, x_free;
     uint64_t s_free, q_full, q_empty, mma_drain, mma_drain2;
     uint32_t tmem_base;
     int32_t abort_flag;
 };
 
 struct Params {
-    const bf16* Q;
-    const bf16* K;
-    const bf16* V;
     bf16* O;
     float scale_log2;
     int q_rows;   // rows of Q seen as [T * h, 128]
@@ -116,13 +128,20 @@ __device__ __forceinline__ void ld_bind(uint32_t (&r)[32]) {
 }
 
 // Steps of the item that query tile t takes part in: the first ones, up to its
-// own last token (none when the unit has no token for the tile).
-__device__ __forceinline__ int tile_steps(const ChunkGeom& u, const ChunkItem& it, int t) {
+// own last token (none when the unit has no token for the tile).  Few rows: every
+// other step, from step t on.
+__device__ __forceinline__ int tile_steps(const ChunkGeom& u, const ChunkItem& it, int t, bool few) {
+    if (few) return (it.s1 - it.s0 + 1 - t) >> 1;
     if (it.nt <= t * u.W) return 0;
     const int hi = it.p0 + min(it.nt, (t + 1) * u.W);
     const int end = min(it.s1, it.sink_tiles + (hi + kBN - 1) / kBN - it.lo_tile);
     return max(0, end - it.s0);
 }
+
+// The kinds of units in the order in which this CTA runs them: every other CTA
+// begins with the few-row units, whose K/V stream from HBM while the others keep
+// the tensor cores busy.
+__device__ __forceinline__ int first_kind() { return blockIdx.x & 1; }
 
 // Bits 0 .. n-1 of a word (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -144,6 +163,215 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t dhi, int t, uin
     for (int kk = 0; kk < kBN / 16; ++kk)
         umma_ts(tmem + kColO + t * 128, tmem + kColP + 64 * t + kk * 8, smem_desc_join(v_lo + (uint32_t)((kk * 2048) >> 4), dhi),
                 idesc, first && kk == 0 ? 0u : 1u);
+}
+
+// Few rows: S^T_t = K(it) Q^T, and O^T_t += V(it)^T P_t with V as an MN-major
+// operand of M = 128 elements of the head and P_t from shared memory.
+__device__ __forceinline__ void issue_st(uint32_t tmem, uint32_t dhi, int t, uint32_t q_lo, uint32_t k_lo) {
+    constexpr uint32_t idesc = idesc_bf16_f32(kBN, kFew, false, false);
+#pragma unroll
+    for (int kk = 0; kk < kD / 16; ++kk) {
+        const uint32_t off = (uint32_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+        umma_ss(tmem + kColS + 64 * t, smem_desc_join(k_lo + off, dhi), smem_desc_join(q_lo + off, dhi), idesc, kk > 0 ? 1u : 0u);
+    }
+}
+__device__ __forceinline__ void issue_pvt(uint32_t tmem, uint32_t dhi, int t, uint32_t v_lo, uint32_t p_lo, bool first) {
+    constexpr uint32_t idesc = idesc_bf16_f32(kD, kFew, true, false);
+#pragma unroll
+    for (int kk = 0; kk < kBN / 16; ++kk)
+        umma_ss(tmem + kColO + t * 128, smem_desc_join(v_lo + (uint32_t)((kk * 2048) >> 4), dhi),
+                smem_desc_join(p_lo + (uint32_t)(((kk >> 2) * kFew * 128 + (kk & 3) * 32) >> 4), dhi), idesc,
+                first && kk == 0 ? 0u : 1u);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// Softmax, epilogue and merge of an item of at most NR rows (few rows), for the
+// warpgroup of tile t.  Each thread holds one key of a step, then one element of
+// the head.  Returns false when a wait ran out.
+template <int NR>
+__device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Smem& sm, const ChunkItem& it, int slot, int t,
+                                         uint32_t tmem, uint32_t& ctile, uint32_t& o_it, uint32_t& votes, uint32_t& swaps) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, col = wq * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + kColS + 64 * t, o_addr = tmem + lane_off + kColO + 128 * t;
+    const int rows = it.nt * u.k, steps = it.s1 - it.s0, n = tile_steps(u, it, t, true);
+    const bool partial = it.rec >= 0;
+    // gate of row `lane`, in flight until the epilogue
+    float gate = 0.f;
+    if (t == 0 && !partial && lane < rows) gate = u.gate[((int64_t)(it.t0 + lane / u.k) * u.g + it.q) * u.k + lane % u.k];
+    float m[NR], l[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+    }
+    // the four warps of the group have written what the others read next
+    auto meet = [&]() {
+        warp_arrive(&sm.vote[t]);
+        const bool ok = warp_wait(sm, u, &sm.vote[t], votes & 1, 46);
+        ++votes;
+        return ok;
+    };
+    for (int i = 0; i < n; ++i, ++ctile) {
+        if (!warp_wait(sm, u, &sm.s_full[t], ctile & 1, 47)) return false;
+        tc_fence_after();
+        uint32_t s[16];
+        tmem_ld16(s_addr, s);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) asm volatile("" : "+r"(s[r]));
+        tc_fence_before();
+        warp_arrive(&sm.st_free[t]);
+        const int kv0 = it.tile(it.s0 + 2 * i + t) * kBN, key = kv0 + col;
+        const bool need_mask = kv0 + kBN - 1 > it.p0 || (u.window && kv0 <= it.hi - 1 - u.window && kv0 + kBN > u.sinks);
+        float x[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(s[r]) * p.scale_log2;
+        if (need_mask) {
+            int pos = it.p0, left = u.k;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (!chunk_sees(u, pos, key)) x[r] = -INFINITY;
+                if (--left == 0) {
+                    left = u.k;
+                    ++pos;
+                }
+            }
+        }
+        float* mine = reinterpret_cast<float*>(sm.wmax[t][votes & 1]) + wq;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float y = warp_max(x[r]);
+            if (lane == 0) mine[4 * r] = y;
+        }
+        const float4* all = sm.wmax[t][votes & 1];
+        if (!meet()) return false;
+        // Lazy rescaling as for many rows; the same for every thread of the group.
+        float alpha[NR];
+        bool rescale = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float4 w = all[r];
+            const float mx = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
+            alpha[r] = 1.f;
+            if (mx > m[r] + kRescaleThreshold || m[r] == -INFINITY) {
+                if (m[r] != -INFINITY) {
+                    alpha[r] = fast_exp2(m[r] - mx);
+                    rescale |= r < rows;
+                }
+                m[r] = mx;
+            }
+        }
+        // P_t and O^T_t: free once the group's previous product has completed
+        if (ctile > 0 && !warp_wait(sm, u, &sm.p_empty[t], (ctile - 1) & 1, 48)) return false;
+        if (rescale) {
+            tc_fence_after();
+            uint32_t o[16];
+            tmem_ld16(o_addr, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int r = 0; r < 16; ++r) asm volatile("" : "+r"(o[r]));
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+                l[r] *= alpha[r];
+            }
+            tmem_st16(o_addr, o);
+            tmem_st_wait();
+        }
+        uint8_t* pt = sm.p[t] + (wq >> 1) * (kFew * 128);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float w = fast_exp2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+            l[r] += w;
+            *reinterpret_cast<bf16*>(pt + r * 128 + (((col & 63) * 2) ^ ((r & 7) << 4))) = __float2bfloat16_rn(w);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(&sm.p_full[t]);
+    }
+    uint32_t o[16];
+    if (n > 0) {
+        if (!warp_wait(sm, u, &sm.o_full[t], o_it & 1, 49)) return false;
+        ++o_it;
+        tc_fence_after();
+        tmem_ld16(o_addr, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) asm volatile("" : "+r"(o[r]));
+        tc_fence_before();
+        warp_arrive(&sm.o_empty[t]);
+        float* mine = reinterpret_cast<float*>(sm.wsum[t]) + wq;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float y = warp_sum(l[r]);
+            if (lane == 0) mine[4 * r] = y;
+        }
+        if (!meet()) return false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float4 w = sm.wsum[t][r];
+            l[r] = (w.x + w.y) + (w.z + w.w);
+        }
+    }
+    if (steps > 1) {  // both groups took part: group 1 hands its state to group 0
+        if (t == 1) {
+            if (!warp_wait(sm, u, &sm.x_free, (swaps & 1) ^ 1, 50)) return false;
+            ++swaps;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                sm.x[r][col] = __uint_as_float(o[r]);
+                if (col == 0) {
+                    sm.x_ml[0][r] = m[r];
+                    sm.x_ml[1][r] = l[r];
+                }
+            }
+            warp_arrive(&sm.x_full);
+            return true;
+        }
+        if (!warp_wait(sm, u, &sm.x_full, swaps & 1, 51)) return false;
+        ++swaps;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float m1 = sm.x_ml[0][r], mx = fmaxf(m[r], m1), ref = mx == -INFINITY ? 0.f : mx;
+            const float a = fast_exp2(m[r] - ref), b = fast_exp2(m1 - ref);  // 0 where a group saw no key
+            o[r] = __float_as_uint(__uint_as_float(o[r]) * a + sm.x[r][col] * b);
+            l[r] = l[r] * a + sm.x_ml[1][r] * b;
+            m[r] = mx;
+        }
+        warp_arrive(&sm.x_free);
+    } else if (t == 1) {
+        return true;
+    }
+    float check = 0.f;  // stays 0, or NaN when a value is not finite
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int head = r < rows ? sm.row_j[slot][0][r] : -1;
+        const float gm = __shfl_sync(0xffffffffu, gate, r);
+        if (head < 0) continue;
+        const float v = __uint_as_float(o[r]);
+        check += v * 0.f + l[r] * 0.f;
+        if (partial) {
+            const bool none = m[r] == -INFINITY && l[r] == 0.f;
+            float* rec = u.part + (int64_t)(it.rec + r) * (kD + 4);
+            rec[col] = none ? 0.f : v / l[r];
+            if (col == 0) rec[kD] = none ? -INFINITY : m[r] + log2f(l[r]);
+        } else {
+            p.O[((int64_t)(it.t0 + r / u.k) * u.h + head) * kD + col] = __float2bfloat16_rn(v * (gm / l[r]));
+        }
+    }
+    if (!(check == 0.f) && !partial) u.odd[u.parts + blockIdx.x] = 1;
+    return true;
 }
 
 // kGather: pages of fewer than 8 rows, fetched row by row.
@@ -174,6 +402,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             mbar_init(&sm.o_full[t], 1);
             mbar_init(&sm.o_empty[t], 4);
         }
+        for (int t = 0; t < kQT; ++t) {
+            mbar_init(&sm.st_free[t], 4);
+            mbar_init(&sm.vote[t], 4);
+        }
+        mbar_init(&sm.x_full, 4);
+        mbar_init(&sm.x_free, 4);
         mbar_init(&sm.s_free, 4);
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
@@ -190,7 +424,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     // above overlaps its tail; nothing it writes is read before this wait.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
-    chunk_split(u, sm.split, blockIdx.x, gridDim.x);  // with block barriers
+    chunk_split(u, sm.split, blockIdx.x);  // with block barriers
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
@@ -207,10 +441,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             tma_prefetch_desc(&mapK);
             tma_prefetch_desc(&mapV);
         }
-        for (uint32_t ui = 0; ok && !aborted(sm); ++ui) {
+        for (uint32_t ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
             const int slot = ui % kItems;
             if (!warp_wait(sm, u, &sm.item_full[slot], (ui / kItems) & 1, 1)) break;
-            if (!sm.has[slot]) break;
+            if (!sm.has[slot]) {
+                warp_arrive(&sm.item_free[slot]);
+                if (++ends == 2) break;
+                continue;
+            }
             const ChunkItem it = sm.item[slot];
             for (int s = it.s0; s < it.s1; ++s, ++kv_it) {
                 const int st = kv_it & 1, kv0 = it.tile(s) * kBN;
@@ -266,21 +504,40 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
             const uint32_t q_lo0 = smem_desc_lo(smem_u32(sm.q[0]), 16), q_lo1 = smem_desc_lo(smem_u32(sm.q[1]), 16);
             const uint32_t k_lo0 = smem_desc_lo(smem_u32(sm.k[0]), 16), k_lo1 = smem_desc_lo(smem_u32(sm.k[1]), 16);
-            uint32_t kv_it = 0, s_cnt = 0;
+            uint32_t kv_it = 0, s_cnt = 0, st_cnt[kQT] = {0, 0};
             bool ok = true;
-            for (uint32_t ui = 0; ok && !aborted(sm); ++ui) {
+            // the S buffer is free: its last reader of either form is done
+            auto s_buffer = [&]() { return s_cnt == 0 || mbar_wait(&sm.s_free, (s_cnt - 1) & 1); };
+            auto st_buffer = [&](int t) { return st_cnt[t] == 0 || mbar_wait(&sm.st_free[t], (st_cnt[t] - 1) & 1); };
+            bool few = first_kind() == 1;
+            uint32_t q_it = 0;
+            for (uint32_t ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
                 const int slot = ui % kItems;
                 if (!mbar_wait(&sm.item_full[slot], (ui / kItems) & 1)) { fail(sm, u, 10); break; }
-                if (!sm.has[slot]) break;
+                if (!sm.has[slot]) {
+                    mbar_arrive(&sm.item_free[slot]);
+                    if (++ends == 2) break;
+                    few = !few;
+                    continue;
+                }
                 const int n = sm.item[slot].s1 - sm.item[slot].s0;
-                const int n0 = tile_steps(u, sm.item[slot], 0), n1 = tile_steps(u, sm.item[slot], 1);
+                const int n0 = tile_steps(u, sm.item[slot], 0, few), n1 = tile_steps(u, sm.item[slot], 1, few);
                 mbar_arrive(&sm.item_free[slot]);
-                if (!mbar_wait(&sm.q_full, ui & 1)) { fail(sm, u, 11); break; }
+                if (!mbar_wait(&sm.q_full, q_it++ & 1)) { fail(sm, u, 11); break; }
+                if (few ? !s_buffer() : !(st_buffer(0) && st_buffer(1))) { fail(sm, u, 14); break; }
                 for (int i = 0; i < n && ok; ++i, ++kv_it) {
                     if (!mbar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1)) { fail(sm, u, 12); ok = false; break; }
-                    for (int t = 0; t < kQT; ++t) {
+                    if (few) {
+                        const int t = i & 1;
+                        if (!st_buffer(t)) { fail(sm, u, 15); ok = false; break; }
+                        tc_fence_after();
+                        issue_st(tmem, dhi, t, q_lo0, (kv_it & 1) ? k_lo1 : k_lo0);
+                        umma_commit(&sm.s_full[t]);
+                        if (t) ++st_cnt[1]; else ++st_cnt[0];
+                    }
+                    for (int t = 0; t < kQT && !few; ++t) {
                         if (i >= (t ? n1 : n0)) continue;
-                        if (s_cnt > 0 && !mbar_wait(&sm.s_free, (s_cnt - 1) & 1)) { fail(sm, u, 13); ok = false; break; }
+                        if (!s_buffer()) { fail(sm, u, 13); ok = false; break; }
                         tc_fence_after();
                         issue_s(tmem, dhi, t ? q_lo1 : q_lo0, (kv_it & 1) ? k_lo1 : k_lo0);
                         umma_commit(&sm.s_full[t]);
@@ -297,68 +554,97 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     } else if (warp == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         // ------------------------------------------------------------ items, row tables, Q
-        ChunkWalk walk(sm.split);
         if (lane == 0) {
             tma_prefetch_desc(&mapQ);
-            u.desc[2 * blockIdx.x].valid = u.desc[2 * blockIdx.x + 1].valid = 0;
+            chunk_clear(u);
         }
-        const int tile_rows = u.W * u.k;
-        int64_t armed = -1;
-        for (uint32_t ui = 0; !aborted(sm); ++ui) {
+        __syncwarp();
+        // this lane's rows 4 lane .. 4 lane + 3 of a tile: token within the tile
+        // (negative: none), selection
+        int tok[4], sel[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = lane * 4 + e;
+            tok[e] = r < u.W * u.k ? r / u.k : INT_MIN / 2;
+            sel[e] = r % u.k;
+        }
+        uint32_t ui = 0, q_it = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int phase = 0; phase < 2 && ok; ++phase) {
+        const bool few = (phase ^ first_kind()) == 1;
+        ChunkWalk walk(u, sm.split, few, blockIdx.x);
+        for (; !aborted(sm); ++ui) {
             const int slot = ui % kItems;
-            if (!warp_wait(sm, u, &sm.item_free[slot], ((ui / kItems) & 1) ^ 1, 20)) break;
+            if (!warp_wait(sm, u, &sm.item_free[slot], ((ui / kItems) & 1) ^ 1, 20)) { ok = false; break; }
             ChunkItem it;
             const bool has = walk.next(u, it);  // the same in every lane
             if (lane == 0) {
                 sm.has[slot] = has;
-                if (has) {
-                    sm.item[slot] = it;
-                    if (chunk_partial(it)) chunk_describe(u, it, blockIdx.x);
-                }
+                if (has) sm.item[slot] = it;
                 mbar_arrive(&sm.item_full[slot]);
             }
-            if (!has) break;
+            if (!has) {  // every barrier of the ring sees every entry
+                warp_arrive(&sm.rows_full[slot]);
+                ++ui;
+                break;
+            }
             const int tiles = it.nt > u.W ? 2 : 1;
-            int row[kQT][4];  // this lane's rows 4 lane .. 4 lane + 3 of each tile, as rows of Q
+            int row[kQT][4];  // the lane's rows of Q
 #pragma unroll
             for (int t = 0; t < kQT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int r = lane * 4 + e, off = t * u.W + r / u.k;
-                    int j = -1;
-                    if (r < tile_rows && off < it.nt) j = chunk_head(u, it.t0 + off, it.q, r % u.k);
-                    sm.row_j[slot][t][r] = j;
-                    row[t][e] = j >= 0 ? (it.t0 + off) * u.h + j : p.q_rows;  // outside: zeros
+                    const int off = tok[e] + t * u.W;
+                    row[t][e] = off >= 0 && off < it.nt ? u.idx[((int64_t)(it.t0 + off) * u.g + it.q) * u.k + sel[e]] : -1;
+                }
+#pragma unroll
+            for (int t = 0; t < kQT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int off = tok[e] + t * u.W, j = row[t][e];
+                    const bool there = off >= 0 && off < it.nt, good = there && j >= it.q * u.hpg && j < (it.q + 1) * u.hpg;
+                    if (there && !good) report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)(it.t0 + off));
+                    sm.row_j[slot][t][lane * 4 + e] = good ? j : -1;
+                    row[t][e] = good ? (it.t0 + off) * u.h + j : p.q_rows;  // outside: zeros
                 }
             warp_arrive(&sm.rows_full[slot]);
-            if (!warp_wait(sm, u, &sm.q_empty, (ui & 1) ^ 1, 21)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, tiles * kTileBytes);
+            if (!warp_wait(sm, u, &sm.q_empty, (q_it & 1) ^ 1, 21)) { ok = false; break; }
+            if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, few ? kFew * kD * 2 : tiles * kTileBytes);
             __syncwarp();
 #pragma unroll
             for (int t = 0; t < kQT; ++t)
-                if (t < tiles) {
+                if (t < tiles && (!few || lane < kFew / 4)) {
                     uint8_t* dst = sm.q[t] + lane * 512;
                     tma_gather4_2d(&mapQ, &sm.q_full, dst, 0, row[t][0], row[t][1], row[t][2], row[t][3]);
                     tma_gather4_2d(&mapQ, &sm.q_full, dst + kHalf, 64, row[t][0], row[t][1], row[t][2], row[t][3]);
                 }
-            armed = ui;
+            ++q_it;
         }
-        if (armed >= 0) mbar_wait(&sm.q_full, armed & 1);  // the last Q loads land before the CTA may exit
+        }
+        if (q_it > 0) mbar_wait(&sm.q_full, (q_it - 1) & 1);  // the last Q loads land before the CTA may exit
     } else if (warp == 3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: O += P V
         const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
         const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v[0]), kHalf), v_lo1 = smem_desc_lo(smem_u32(sm.v[1]), kHalf);
+        const uint32_t p_lo0 = smem_desc_lo(smem_u32(sm.p[0]), 16), p_lo1 = smem_desc_lo(smem_u32(sm.p[1]), 16);
         const int page = 1 << u.page_shift;
         uint32_t kv_it = 0, c[kQT] = {0, 0}, o_cnt[kQT] = {0, 0};
         bool ok = true;
-        for (uint32_t ui = 0; ok && !aborted(sm); ++ui) {
+        bool few = first_kind() == 1;
+        for (uint32_t ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
             const int slot = ui % kItems;
             if (!warp_wait(sm, u, &sm.item_full[slot], (ui / kItems) & 1, 30)) break;
-            if (!sm.has[slot]) break;
+            if (!sm.has[slot]) {
+                warp_arrive(&sm.item_free[slot]);
+                if (++ends == 2) break;
+                few = !few;
+                continue;
+            }
             const ChunkItem it = sm.item[slot];
             warp_arrive(&sm.item_free[slot]);
-            const int n = it.s1 - it.s0, n0 = tile_steps(u, it, 0), n1 = tile_steps(u, it, 1);
+            const int n = it.s1 - it.s0, n0 = tile_steps(u, it, 0, few), n1 = tile_steps(u, it, 1, few);
             for (int i = 0; i < n && ok; ++i, ++kv_it) {
                 if (!warp_wait(sm, u, &sm.kv_full_v[kv_it & 1], (kv_it >> 1) & 1, 31)) { ok = false; break; }
                 // Rows of loaded pages that no row of the unit sees: past the last
@@ -382,17 +668,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     __syncwarp();
                 }
                 for (int t = 0; t < kQT; ++t) {
-                    if (i >= (t ? n1 : n0)) continue;
+                    const int j = few ? i >> 1 : i;  // the group's own step
+                    if (few ? (i & 1) != t : i >= (t ? n1 : n0)) continue;
                     if (!warp_wait(sm, u, &sm.p_full[t], c[t] & 1, 32)) { ok = false; break; }
-                    if (i == 0 && !warp_wait(sm, u, &sm.o_empty[t], (o_cnt[t] & 1) ^ 1, 33)) { ok = false; break; }
+                    if (j == 0 && !warp_wait(sm, u, &sm.o_empty[t], (o_cnt[t] & 1) ^ 1, 33)) { ok = false; break; }
                     if (lane == 0) {
                         tc_fence_after();
-                        issue_pv(tmem, dhi, t, (kv_it & 1) ? v_lo1 : v_lo0, i == 0);
+                        const uint32_t v_lo = (kv_it & 1) ? v_lo1 : v_lo0;
+                        if (few)
+                            issue_pvt(tmem, dhi, t, v_lo, t ? p_lo1 : p_lo0, j == 0);
+                        else
+                            issue_pv(tmem, dhi, t, v_lo, j == 0);
                         umma_commit(&sm.p_empty[t]);
-                        if (i == (t ? n1 : n0) - 1) umma_commit(&sm.o_full[t]);
+                        if (j == (t ? n1 : n0) - 1) umma_commit(&sm.o_full[t]);
                     }
                     ++c[t];
-                    if (i == 0) ++o_cnt[t];
+                    if (j == 0) ++o_cnt[t];
                 }
                 if (!ok) break;
                 if (lane == 0) umma_commit(&sm.kv_empty_v[kv_it & 1]);
@@ -417,35 +708,62 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const int sel = r % u.k;
         const bool in_tile = r < u.W * u.k;
         const uint64_t C2 = pk2(p.scale_log2, p.scale_log2);
-        uint32_t ctile = 0, o_it = 0;
-        for (uint32_t ui = 0; !aborted(sm); ++ui) {
+        uint32_t ctile = 0, o_it = 0, votes = 0, swaps = 0;
+        uint32_t ui = 0;
+        // The next item of the kind, or null at its end (or after a failure).
+        auto take = [&]() -> const ChunkItem* {
+            if (aborted(sm) || !warp_wait(sm, u, &sm.item_full[ui % kItems], (ui / kItems) & 1, 40)) return nullptr;
+            if (sm.has[ui % kItems]) return &sm.item[ui % kItems];
+            warp_arrive(&sm.item_free[ui++ % kItems]);
+            return nullptr;
+        };
+        auto done = [&]() { warp_arrive(&sm.item_free[ui++ % kItems]); };
+        // The unselected output slots of the tile's tokens, by the part that holds
+        // the unit's first step.
+        auto zero_fill = [&](const ChunkItem& it, int toks) {
+            if (it.s0 != 0 || u.k == u.hpg) return;
+            const int32_t* heads = sm.row_j[ui % kItems][t];
+            for (int x = wq * 32 + lane; x < toks * u.hpg * 16; x += 128) {
+                const int j = it.q * u.hpg + (x >> 4) % u.hpg, tok = (x >> 4) / u.hpg;
+                bool chosen = false;
+                for (int a = 0; a < u.k; ++a) chosen |= heads[tok * u.k + a] == j;
+                if (!chosen)
+                    *reinterpret_cast<uint4*>(p.O + ((int64_t)(it.t0 + t * u.W + tok) * u.h + j) * kD + (x & 15) * 8) =
+                        make_uint4(0, 0, 0, 0);
+            }
+        };
+#pragma unroll 1
+        for (int phase = 0; phase < 2; ++phase) {
+        if ((phase ^ first_kind()) == 1) {
+            while (const ChunkItem* next = take()) {
+                const ChunkItem it = *next;
+                const int slot = ui % kItems;
+                if (!warp_wait(sm, u, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
+                if (t == 0) zero_fill(it, it.nt);
+                if (!(it.nt * u.k <= 4 ? few_item<4>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)
+                                       : few_item<16>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)))
+                    break;
+                done();
+            }
+            continue;
+        }
+        while (const ChunkItem* next = take()) {
+            const ChunkItem it = *next;
             const int slot = ui % kItems;
-            if (!warp_wait(sm, u, &sm.item_full[slot], (ui / kItems) & 1, 40)) break;
-            if (!sm.has[slot]) break;
-            const ChunkItem it = sm.item[slot];
-            const int n = tile_steps(u, it, t);
+            const int n = tile_steps(u, it, t, false);
             const int toks = min(it.nt - t * u.W, u.W);  // of this tile; 0 or less: none
+            // Every item's rows_full phase is waited for in turn, as a later one may
+            // complete before a waiter of the same parity looks.
+            if (!warp_wait(sm, u, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
             if (toks <= 0) {
-                warp_arrive(&sm.item_free[slot]);
+                done();
                 continue;
             }
-            const bool partial = chunk_partial(it);
+            const bool partial = it.rec >= 0;
             const bool mine = in_tile && off < it.nt;
             const int token = it.t0 + off;
             const float gate = mine ? u.gate[((int64_t)token * u.g + it.q) * u.k + sel] : 0.f;
-            if (!warp_wait(sm, u, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
-            // The unselected output slots of the tile's tokens, by the part that
-            // holds the unit's first step.
-            if (it.s0 == 0 && u.k < u.hpg) {
-                for (int x = wq * 32 + lane; x < toks * u.hpg * 16; x += 128) {
-                    const int j = it.q * u.hpg + (x >> 4) % u.hpg, tok = (x >> 4) / u.hpg;
-                    bool chosen = false;
-                    for (int a = 0; a < u.k; ++a) chosen |= sm.row_j[slot][t][tok * u.k + a] == j;
-                    if (!chosen)
-                        *reinterpret_cast<uint4*>(p.O + ((int64_t)(it.t0 + t * u.W + tok) * u.h + j) * kD + (x & 15) * 8) =
-                            make_uint4(0, 0, 0, 0);
-                }
-            }
+            zero_fill(it, toks);
             const int head = mine ? sm.row_j[slot][t][r] : -1;
             const bool live = wq * 32 < toks * u.k;  // some row of this warp is a query row
             // Keys this row sees: [low, pos] and those below u.sinks.  A padding row
@@ -599,17 +917,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             if (!ok) break;
             // Epilogue: O_t / l, gated, as the bf16 row of O, or the row's partial
             // record (o, log2-sum-exp); none of this part's keys seen: -inf.
-            float* rec = u.part + ((int64_t)chunk_slot(it, blockIdx.x) * u.row_cap + t * u.W * u.k + r) * (kD + 4);
+            float* rec = u.part + (int64_t)(it.rec + t * u.W * u.k + r) * (kD + 4);
             if (n == 0) {
                 if (partial && mine) rec[kD] = -INFINITY;
-                warp_arrive(&sm.item_free[slot]);
+                done();
                 continue;
             }
             if (!warp_wait(sm, u, &sm.o_full[t], o_it & 1, 44)) break;
             ++o_it;
             if (!live) {
                 warp_arrive(&sm.o_empty[t]);
-                warp_arrive(&sm.item_free[slot]);
+                done();
                 continue;
             }
             tc_fence_after();
@@ -629,8 +947,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) check[e & 3] = fmaf(__uint_as_float(o[cb][e]), 0.f, check[e & 3]);
-            const bool redo = head >= 0 && !((check[0] + check[1]) + (check[2] + check[3]) == 0.f);
-            if (head >= 0 && !redo) {
+            if (head >= 0) {
+                if (!partial && !((check[0] + check[1]) + (check[2] + check[3]) == 0.f)) u.odd[blockIdx.x] = 1;
                 if (partial) {
 #pragma unroll
                     for (int cb = 0; cb < 4; ++cb)
@@ -655,15 +973,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         }
                 }
             }
-            for (unsigned again = __ballot_sync(0xffffffffu, redo); again; again &= again - 1) {
-                const int src = __ffs(again) - 1;
-                const int jj = __shfl_sync(0xffffffffu, head, src), tok = __shfl_sync(0xffffffffu, token, src);
-                const int pp = __shfl_sync(0xffffffffu, pos, src);
-                float a2[kD / 32], m2, l2;
-                chunk_row<bf16, kD>(u, it, pp, p.Q + ((int64_t)tok * u.h + jj) * kD, p.K, p.V, p.scale_log2, a2, m2, l2);
-                chunk_store_row<bf16, kD>(u, it, blockIdx.x, t * u.W * u.k + wq * 32 + src, tok, jj, a2, m2, l2, p.O);
-            }
-            warp_arrive(&sm.item_free[slot]);
+            done();
+        }
         }
     }
 
@@ -678,9 +989,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
 
 }  // namespace
 
-ChunkTiling chunk_tc_tiling() { return {kBM, kQT, kBN, 2 * kBN, 4 * kBN, 1}; }
+ChunkTiling chunk_tc_tiling() { return {kBM, kQT, kFew, kBN, 2 * kBN, 4 * kBN, 1}; }
 
-cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a, int parts) {
+cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
     const gqe_shape& s = *a.s;
     // The setmaxnreg split needs exactly kRegsLaunch registers per thread at
     // launch (a property of the compiled kernels: checked once per process).
@@ -716,9 +1027,6 @@ cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a, int parts) {
     if (!make_bf16_map(&mapQ, a.Q, 2, qdims, &row_bytes, row_box)) return cudaErrorInvalidValue;
 
     Params p;
-    p.Q = (const bf16*)a.Q;
-    p.K = (const bf16*)a.K_pages;
-    p.V = (const bf16*)a.V_pages;
     p.O = (bf16*)a.O;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)kD);
     p.q_rows = (int)q_rows;
@@ -728,7 +1036,7 @@ cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a, int parts) {
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(parts);
+    cfg.gridDim = dim3(u.parts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
