@@ -133,8 +133,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the current stream's handle (a torch Stream object costs 3 us to make)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -294,51 +294,71 @@ def gqe_aux_loss(shape, logits, idx, loss, dlogits, workspace, stream=None) -> N
                                              _ptr(dlogits), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
-def _tensors(fn, *specs):
-    """Refuse (GQE_ERR_INVALID_ARGUMENT) a tensor that is not on the current
-    device, or not of the dtype, shape and dense layout the call reads it with.
-    specs: (tensor, dtype, shape)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for t, dtype, shape in specs:
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.device.index != dev:
+def _device(fn, t):
+    """The current device, if t is on it; else the call is refused."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
+    return dev
+
+
+def _dense(fn, dev, dtype, n, *tensors):
+    """Refuse a tensor that is not n dense elements of dtype on device dev."""
+    for t in tensors:
+        if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
             raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
-
-
-def _shape_dtype(shape: GqeShape):
-    return torch.bfloat16 if shape.dtype == GQE_BF16 else torch.float32
 
 
 def gqe_page_plan(page_size, lengths, new_lens, free_pages, free_count, block_table, lengths_out, free_count_out,
                   cu_new, slots, workspace, stream=None) -> None:
     """n_seqs, rows, num_pages and max_blocks are the sizes of lengths, slots,
     free_pages and block_table's rows."""
-    n, i32 = lengths.numel(), torch.int32
-    _tensors("gqe_page_plan", (lengths, i32, (n,)), (new_lens, i32, (n,)), (free_pages, i32, (free_pages.numel(),)),
-             (free_count, i32, (1,)), (block_table, i32, (n, block_table.shape[-1])), (lengths_out, i32, (n,)),
-             (free_count_out, i32, (1,)), (cu_new, i32, (n + 1,)), (slots, i32, (slots.numel(),)),
-             (workspace, torch.uint8, workspace.shape))
-    _check("gqe_page_plan", _lib.gqe_page_plan(
-        n, slots.numel(), int(page_size), free_pages.numel(), block_table.shape[1], lengths.data_ptr(),
-        new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), block_table.data_ptr(),
-        lengths_out.data_ptr(), free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _stream(stream)))
+    fn, i32 = "gqe_page_plan", torch.int32
+    n, rows, pages, blocks, nbytes = (lengths.numel(), slots.numel(), free_pages.numel(), block_table.shape[-1],
+                                      workspace.numel())
+    dev = _device(fn, lengths)
+    _dense(fn, dev, i32, n, lengths, new_lens, lengths_out)
+    _dense(fn, dev, i32, 1, free_count, free_count_out)
+    _dense(fn, dev, i32, n * blocks, block_table)
+    _dense(fn, dev, i32, n + 1, cu_new)
+    _dense(fn, dev, i32, rows, slots)
+    _dense(fn, dev, i32, pages, free_pages)
+    _dense(fn, dev, torch.uint8, nbytes, workspace)
+    _check(fn, _lib.gqe_page_plan(
+        n, rows, int(page_size), pages, blocks, lengths.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+        free_count.data_ptr(), block_table.data_ptr(), lengths_out.data_ptr(), free_count_out.data_ptr(),
+        cu_new.data_ptr(), slots.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
+
+
+def _pages(fn, dev, shape, dtype, K_pages, V_pages):
+    """(num_pages, page_size) of the page pools."""
+    dims = K_pages.shape
+    if len(dims) != 4 or dims[2] != shape.g or dims[3] != shape.d_h or V_pages.shape != dims:
+        raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
+    _dense(fn, dev, dtype, K_pages.numel(), K_pages, V_pages)
+    return dims[0], dims[1]
 
 
 def gqe_kv_append(shape, K_new, V_new, slots, K_pages, V_pages, workspace, stream=None) -> None:
     """K_new and V_new [rows, g, d_h] may have any row stride that keeps rows
     16-byte aligned (slices of a fused projection's output)."""
-    fn, dt, g, d = "gqe_kv_append", _shape_dtype(shape), shape.g, shape.d_h
-    rows = shape.B * shape.T
-    _tensors(fn, (slots, torch.int32, (rows,)), (K_pages, dt, (*K_pages.shape[:2], g, d)), (V_pages, dt, K_pages.shape),
-             (workspace, torch.uint8, workspace.shape))
+    fn, dt, g, d = "gqe_kv_append", torch.bfloat16 if shape.dtype == GQE_BF16 else torch.float32, shape.g, shape.d_h
+    rows, nbytes = shape.B * shape.T, workspace.numel()
+    dev = _device(fn, slots)
+    _dense(fn, dev, torch.int32, rows, slots)
+    _dense(fn, dev, torch.uint8, nbytes, workspace)
+    pages, page_size = _pages(fn, dev, shape, dt, K_pages, V_pages)
+    strides = []
     for t in (K_new, V_new):
-        if (t.dtype != dt or t.shape != (rows, g, d) or t.stride(2) != 1 or (g > 1 and t.stride(1) != d)
-                or t.device != slots.device):
+        if t.dtype is not dt or t.shape != (rows, g, d) or t.get_device() != dev:
             raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
-    _check(fn, _lib.gqe_kv_append(ctypes.byref(shape), K_new.data_ptr(), K_new.stride(0), V_new.data_ptr(),
-                                  V_new.stride(0), slots.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
-                                  K_pages.shape[0], K_pages.shape[1], workspace.data_ptr(), workspace.numel(),
-                                  _stream(stream)))
+        st = t.stride()
+        if st[2] != 1 or (g > 1 and st[1] != d):
+            raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
+        strides.append(st[0])
+    _check(fn, _lib.gqe_kv_append(ctypes.byref(shape), K_new.data_ptr(), strides[0], V_new.data_ptr(), strides[1],
+                                  slots.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), pages, page_size,
+                                  workspace.data_ptr(), nbytes, _stream(stream)))
 
 
 def gqe_chunk_workspace_bytes(shape) -> int:
@@ -348,21 +368,24 @@ def gqe_chunk_workspace_bytes(shape) -> int:
 def gqe_attn_chunk_paged(shape, Q, K_pages, V_pages, block_table, cu_new, lengths, window, sinks, idx, gate, O,
                          workspace, stream=None) -> None:
     """n_seqs, max_blocks, num_pages and page_size are the sizes of lengths,
-    block_table's rows and K_pages; tensors may carry a leading batch of 1."""
-    fn, dt, T, g, d = "gqe_attn_chunk_paged", _shape_dtype(shape), shape.T, shape.g, shape.d_h
-    n, i32 = lengths.numel(), torch.int32
-    rows = (T, shape.h, d) if Q.dim() == 3 else (1, T, shape.h, d)
-    sel = (T, g, shape.k) if idx.dim() == 3 else (1, T, g, shape.k)
-    _tensors(fn, (Q, dt, rows), (O, dt, O.shape if O.numel() == Q.numel() else rows), (idx, i32, sel),
-             (gate, torch.float32, gate.shape if gate.numel() == idx.numel() else sel),
-             (K_pages, dt, (*K_pages.shape[:2], g, d)), (V_pages, dt, K_pages.shape),
-             (block_table, i32, (n, block_table.shape[-1])), (cu_new, i32, (n + 1,)), (lengths, i32, (n,)),
-             (workspace, torch.uint8, workspace.shape))
+    block_table's rows and K_pages; Q, O, idx and gate are read as dense
+    [T, h, d_h] and [T, g, k] (a leading batch of 1 is fine)."""
+    fn, dt, T = "gqe_attn_chunk_paged", torch.bfloat16 if shape.dtype == GQE_BF16 else torch.float32, shape.T
+    n, blocks, nbytes, i32 = lengths.numel(), block_table.shape[-1], workspace.numel(), torch.int32
+    dev = _device(fn, Q)
+    _dense(fn, dev, dt, T * shape.h * shape.d_h, Q, O)
+    picks = T * shape.g * shape.k
+    _dense(fn, dev, i32, picks, idx)
+    _dense(fn, dev, torch.float32, picks, gate)
+    _dense(fn, dev, i32, n, lengths)
+    _dense(fn, dev, i32, n + 1, cu_new)
+    _dense(fn, dev, i32, n * blocks, block_table)
+    _dense(fn, dev, torch.uint8, nbytes, workspace)
+    pages, page_size = _pages(fn, dev, shape, dt, K_pages, V_pages)
     _check(fn, _lib.gqe_attn_chunk_paged(
-        ctypes.byref(shape), Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), K_pages.shape[0], K_pages.shape[1],
-        block_table.data_ptr(), block_table.shape[1], n, cu_new.data_ptr(), lengths.data_ptr(), int(window),
-        int(sinks), idx.data_ptr(), gate.data_ptr(), O.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _stream(stream)))
+        ctypes.byref(shape), Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), pages, page_size,
+        block_table.data_ptr(), blocks, n, cu_new.data_ptr(), lengths.data_ptr(), int(window), int(sinks),
+        idx.data_ptr(), gate.data_ptr(), O.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
 
 
 def gqe_get_device_status(workspace, stream=None) -> int:
@@ -476,7 +499,7 @@ class PagedCache:
     def __init__(self, shape: GqeShape, n_seqs: int, num_pages: int, page_size: int, max_blocks: int, layers: int = 1,
                  device="cuda"):
         self.shape, self.page_size = shape, int(page_size)
-        dt = _shape_dtype(shape)
+        dt = torch.bfloat16 if shape.dtype == GQE_BF16 else torch.float32
         i32 = dict(dtype=torch.int32, device=device)
         pages = (num_pages, page_size, shape.g, shape.d_h)
         self.K_pages = [torch.empty(pages, dtype=dt, device=device) for _ in range(layers)]

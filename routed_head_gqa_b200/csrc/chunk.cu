@@ -161,9 +161,7 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     u.BN = t.keys;
     u.bn_shift = 0;
     while ((1 << u.bn_shift) < t.keys) ++u.bn_shift;
-    u.unit_keys = t.unit_keys;
-    u.per_min = 1.0f / t.min_cost;
-    u.few = t.few;
+    u.few_tokens = t.few / s.k;
     u.parts = parts;
     u.row_cap = row_cap(&s, t);
     u.few_cap = few_cap(&s, t);
@@ -171,6 +169,17 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     u.window = a.window >= u.cap ? 0 : a.window;
     u.sinks = u.window == 0 ? 0 : a.sinks < u.cap ? a.sinks : u.cap;
     u.page_shift = a.page_shift;
+    const int page = 1 << a.page_shift;
+    u.align = page < 8 ? 8 : page < t.keys ? page : t.keys;
+    // No more than one unit per token, nor than the full ones and one per request.
+    int64_t units = (s.T + u.WU - 1) / u.WU + (int64_t)a.n_seqs;
+    if (units > s.T) units = s.T;
+    u.cost_shift = 4;
+    while ((units * s.g * ((int64_t)u.cap + u.WU + t.unit_keys) >> u.cost_shift) + units * s.g >= ((int64_t)1 << 31))
+        ++u.cost_shift;
+    u.unit_cost = t.unit_keys >> u.cost_shift > 0 ? t.unit_keys >> u.cost_shift : 1;
+    const int least = t.min_keys >> u.cost_shift;
+    u.per_min = 1.0f / (least > 0 ? least : 1);
     u.num_pages = a.num_pages;
     u.max_blocks = a.max_blocks;
     u.cu = a.cu_new;

@@ -9,8 +9,9 @@
 // WU consecutive new tokens) holds k * WU query rows, row r being token r / k,
 // selection r % k: no compaction lists, and a unit's rows differ in position by
 // less than WU, which keeps the masked band narrow.  A unit walks its visible
-// keys in steps of BN: the tiles of the first `sinks` keys that lie below the
-// window, then the tiles from the window's lower edge to the last token.
+// cache rows in steps of BN: the pages of the first `sinks` keys, then, closed up
+// behind them, those from the window's lower edge to the last token, so that a
+// few first keys cost a page of a step and not a step.
 //
 // Schedule.  The lengths live on the device, so the grid cannot be cut on the
 // host.  Every CTA instead derives the same split of the whole step: a cost per
@@ -41,9 +42,11 @@ struct ChunkGeom {
     int T, n_seqs, h, g, k, hpg;
     int W, WU;        // tokens per query tile and per unit
     int BN, bn_shift; // keys per step and their log2
-    int unit_keys;    // a unit's fixed cost, in keys
-    float per_min;    // 1 / the smallest cost worth a part, in keys
-    int few;          // query rows up to which a request is of the second kind
+    int align;        // rows that the parts of a unit's key list are aligned to
+    int cost_shift;   // costs are counted in 2^cost_shift keys, so that a step's total fits 32 bits
+    uint32_t unit_cost;  // a unit's fixed cost
+    float per_min;    // 1 / the smallest cost worth a part
+    int few_tokens;   // new tokens up to which a request is of the second kind
     int parts;        // CTAs, and parts of either kind at most
     int row_cap, few_cap;  // query rows that the partial records of a unit take, by kind
     int window, sinks;
@@ -64,12 +67,11 @@ struct ChunkItem {
     int b, q;
     int t0, nt;            // first packed token and the number of tokens
     int p0;                // position of token t0
-    int sink_tiles;        // steps 0 .. sink_tiles-1 are tiles 0 ..
-    int lo_tile;           // steps sink_tiles .. are tiles lo_tile ..
     int lo, hi;            // keys [lo, hi) and, below lo, keys < sinks are seen by some row
+    int head, skip;        // list row x is key x for x < head, else key x + skip
     int steps, s0, s1;     // the unit's steps and this part's [s0, s1)
     int rec;               // the unit's first partial record if it is split, else -1
-    __device__ __forceinline__ int tile(int s) const { return s < sink_tiles ? s : lo_tile + (s - sink_tiles); }
+    __device__ __forceinline__ int key(int x) const { return x < head ? x : x + skip; }
 };
 
 struct ChunkSeq {
@@ -99,24 +101,26 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkGeom& u, int b) {
 }
 
 // 0: many query rows, 1: few.
-__device__ __forceinline__ int chunk_kind(const ChunkGeom& u, int n) { return n <= u.few / u.k ? 1 : 0; }
+__device__ __forceinline__ int chunk_kind(const ChunkGeom& u, int n) { return n <= u.few_tokens ? 1 : 0; }
 
 __device__ __forceinline__ int chunk_units(const ChunkGeom& u, int n) { return (n + u.WU - 1) / u.WU; }
 
-// Cost of the first i units of a request and group, in keys, in closed form:
-// unit j sees about first + j * WU keys, or the window's span if that is less.
-__device__ __forceinline__ int64_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s, int i) {
-    const int first = s.L - s.n + min(s.n, u.WU);
-    int64_t cost = (int64_t)i * u.unit_keys;
-    int grow = i;
+// Cost of the first i units of a request and group in closed form: unit j sees
+// about first + j * WU keys, or the window's span if that is less.
+__device__ __forceinline__ uint32_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s, int i) {
+    const uint32_t first = s.L - s.n + min(s.n, u.WU);
+    uint32_t grow = i;
+    uint64_t keys = 0;
     if (u.window) {
-        const int64_t span = (int64_t)u.window + u.WU + u.sinks;  // below 2^32: window and sinks are at most 2^30
-        grow = first < span ? min((uint32_t)i, ((uint32_t)(span - first) + u.WU - 1) / (uint32_t)u.WU) : 0;
-        cost += (i - grow) * span;
+        const uint32_t span = (uint32_t)u.window + u.WU + u.sinks;  // window and sinks are at most 2^30
+        grow = first < span ? min((uint32_t)i, (span - first + u.WU - 1) / (uint32_t)u.WU) : 0;
+        keys = (uint64_t)(i - grow) * span;
     }
-    return cost + (int64_t)grow * first + u.WU * ((int64_t)grow * (grow - 1) / 2);
+    keys += (uint64_t)grow * first;
+    if (grow > 1) keys += (uint64_t)u.WU * ((uint64_t)grow * (grow - 1) / 2);
+    return (uint32_t)(keys >> u.cost_shift) + i * u.unit_cost;
 }
-__device__ __forceinline__ int64_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s) {
+__device__ __forceinline__ uint32_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s) {
     return s.n > 0 ? u.g * chunk_cost(u, s, chunk_units(u, s.n)) : 0;
 }
 
@@ -128,10 +132,17 @@ __device__ __forceinline__ void chunk_item(const ChunkGeom& u, const ChunkSeq& s
     it.nt = min(u.WU, s.n - first);
     it.p0 = s.L - s.n + first;
     it.hi = it.p0 + it.nt;
-    it.lo = u.window ? max(0, it.p0 - u.window + 1) : 0;
-    it.lo_tile = it.lo >> u.bn_shift;
-    it.sink_tiles = min(it.lo_tile, (min(u.sinks, it.lo) + u.BN - 1) >> u.bn_shift);
-    it.steps = it.sink_tiles + ((it.hi + u.BN - 1) >> u.bn_shift) - it.lo_tile;
+    it.lo = it.head = it.skip = 0;
+    if (u.window) {
+        it.lo = max(0, it.p0 - u.window + 1);
+        const int from = it.lo & ~(u.align - 1);
+        const int head = (min(u.sinks, it.lo) + u.align - 1) & ~(u.align - 1);
+        if (head < from) {  // else the two parts touch: the list is the keys from 0 on
+            it.head = head;
+            it.skip = from - head;
+        }
+    }
+    it.steps = (it.hi - it.skip + u.BN - 1) >> u.bn_shift;
 }
 
 // Whether a row at position p sees key s.
@@ -147,22 +158,27 @@ struct ChunkPlace {
 // Where a cost `rest` (within request b's own cost) falls.  The quotients are
 // taken in fp32: they only place the boundaries, and the two parts that meet at
 // one evaluate the same expression.
-__device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const ChunkSeq& s, int b, int64_t rest) {
+__device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const ChunkSeq& s, int b, uint32_t rest) {
     const int units = chunk_units(u, s.n);
-    const int64_t per = chunk_cost(u, s, units);
+    const uint32_t per = chunk_cost(u, s, units);
     ChunkPlace pl;
     pl.b = b;
     pl.q = min((int)__fdividef((float)rest, (float)per), u.g - 1);
-    if (pl.q > 0 && rest < pl.q * per) --pl.q;
+    if (rest < pl.q * per) --pl.q;
     if (pl.q + 1 < u.g && rest >= (pl.q + 1) * per) ++pl.q;
     rest -= pl.q * per;
-    int lo = 0, hi = units - 1;  // the last unit whose prefix does not exceed rest
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (chunk_cost(u, s, mid) <= rest) lo = mid; else hi = mid - 1;
+    int lo = 0;
+    uint32_t before = 0, cost = per;
+    if (units > 1) {
+        int hi = units - 1;  // the last unit whose prefix does not exceed rest
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (chunk_cost(u, s, mid) <= rest) lo = mid; else hi = mid - 1;
+        }
+        before = chunk_cost(u, s, lo);
+        cost = chunk_cost(u, s, lo + 1) - before;
     }
     pl.i = lo;
-    const int64_t before = chunk_cost(u, s, lo), cost = chunk_cost(u, s, lo + 1) - before;
     ChunkItem it;
     chunk_item(u, s, b, pl.q, lo, it);
     pl.s = max(0, min((int)(__fdividef((float)(rest - before), (float)cost) * it.steps), it.steps - 1));
@@ -171,7 +187,7 @@ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const Chun
 
 // Shared state of the split: filled by chunk_split, read by the item walk.
 struct ChunkSplit {
-    int64_t warp_sum[2][32];
+    uint32_t warp_sum[2][32];
     ChunkPlace from[2], to[2];  // by kind
 };
 
@@ -186,32 +202,35 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
     const int per = (u.n_seqs + blockDim.x - 1) / blockDim.x;
     const int b0 = min(tid * per, u.n_seqs), b1 = min(b0 + per, u.n_seqs);
     ChunkSeq only;  // the request of a thread that has one
-    int64_t mine[2] = {0, 0};
+    uint32_t mine[2] = {0, 0};
     for (int b = b0; b < b1; ++b) {
         only = chunk_seq(u, b);
-        const int64_t cost = chunk_cost(u, only);
+        const uint32_t cost = chunk_cost(u, only);
         if (chunk_kind(u, only.n)) mine[1] += cost; else mine[0] += cost;
     }
     if (tid < 2) {  // overwritten below where the place exists
         sp.from[tid] = {u.n_seqs, 0, 0, 0};
         sp.to[tid] = {u.n_seqs, 0, 0, 0};
     }
-    int64_t run[2];
+    uint32_t run[2] = {mine[0], mine[1]};
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-        run[kind] = mine[kind];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, run[kind], d);
-            if (lane >= d) run[kind] += o;
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, run[0], d), y = __shfl_up_sync(0xffffffffu, run[1], d);
+        if (lane >= d) {
+            run[0] += x;
+            run[1] += y;
         }
-        if (lane == 31) sp.warp_sum[kind][warp] = run[kind];
+    }
+    if (lane == 31) {
+        sp.warp_sum[0][warp] = run[0];
+        sp.warp_sum[1][warp] = run[1];
     }
     __syncthreads();
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
-        const int64_t own = kind ? mine[1] : mine[0];
-        int64_t before = (kind ? run[1] : run[0]) - own, total = 0;
+        const uint32_t own = kind ? mine[1] : mine[0];
+        if (own == 0) continue;
+        uint32_t before = (kind ? run[1] : run[0]) - own, total = 0;
         for (int w = 0; w < nw; ++w) {
             if (w < warp) before += sp.warp_sum[kind][w];
             total += sp.warp_sum[kind][w];
@@ -219,18 +238,17 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
         const float want = (float)total * u.per_min;
         const int parts = want < 1.f ? 1 : want > (float)u.parts ? u.parts : (int)want;
         const int c = chunk_part(u, kind, cta);
-        if (c >= parts || own == 0) continue;
+        if (c >= parts) continue;
 #pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            if (c + e == parts) break;  // the last part ends with the step
+        for (int e = 0; e < 2 && c + e < parts; ++e) {  // the last part ends with the step
             const uint32_t frac = (uint32_t)(__fdiv_rn((float)(c + e), (float)parts) * 4294967296.f);
-            const int64_t x = (total >> 32) * frac + (int64_t)(((uint64_t)(uint32_t)total * frac) >> 32);  // total * (c + e) / parts
-            if (x < before || x >= before + own) continue;
-            int64_t at = before;
+            const uint32_t x = __umulhi(total, frac);  // total * (c + e) / parts
+            if (x < before || x - before >= own) continue;
+            uint32_t at = before;
             for (int b = b0; b < b1; ++b) {
                 const ChunkSeq s = per == 1 ? only : chunk_seq(u, b);
-                const int64_t cost = chunk_kind(u, s.n) == kind ? chunk_cost(u, s) : 0;
-                if (x < at + cost) {
+                const uint32_t cost = chunk_kind(u, s.n) == kind ? chunk_cost(u, s) : 0;
+                if (x - at < cost) {
                     const ChunkPlace pl = chunk_place(u, s, b, x - at);
                     if (e) sp.to[kind] = pl; else sp.from[kind] = pl;
                     break;
@@ -339,8 +357,9 @@ __device__ __forceinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& i
     }
     m = -INFINITY;
     l = 0.f;
-    for (int st = 0; st < it.steps; ++st) {
-        const int k0 = it.tile(st) * u.BN, k1 = min(k0 + u.BN, p + 1);
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+        const int k0 = part ? it.head + it.skip : 0, k1 = part ? p + 1 : it.head;
         for (int s = k0; s < k1; s += 4) {  // four keys' loads in flight
             float x[4], v[4][D / 32];
             bool on[4];
@@ -405,7 +424,7 @@ cudaError_t launch_chunk(const ChunkArgs& a);
 // to which a request is of the second kind, keys per step, a unit's fixed cost and
 // the smallest part in keys, blocks per SM.
 struct ChunkTiling {
-    int rows, tiles, few, keys, unit_keys, min_cost, per_sm;
+    int rows, tiles, few, keys, unit_keys, min_keys, per_sm;
 };
 ChunkTiling chunk_simt_tiling();
 cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a);

@@ -40,9 +40,8 @@ template <typename T, int D>
 __device__ __forceinline__ void load_tile(const ChunkGeom& u, const ChunkItem& it, int step, const T* pages, T* dst) {
     using C = SimtCfg<T, D>;
     constexpr int kPer = D / C::kVec;  // 16-byte vectors per row
-    const int k0 = it.tile(step) * kBN;
     for (int v = threadIdx.x; v < kBN * kPer; v += kThreads) {
-        const int row = v / kPer, x = (v % kPer) * C::kVec, s = k0 + row;
+        const int row = v / kPer, x = (v % kPer) * C::kVec, s = it.key(step * kBN + row);
         const bool on = s < it.hi && (s >= it.lo || s < u.sinks);
         const T* src = pages;
         if (on) src += (chunk_cache_row(u, it.b, s) * u.g + it.q) * D + x;
@@ -173,13 +172,15 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
         __syncthreads();  // every thread has read K
         if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Kp, Ks);
         cp_async_commit();
-        const int k0 = it.tile(st) * kBN;
+        int key[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) key[j] = it.key(st * kBN + tx + 16 * j);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] = chunk_sees(u, pos[i], k0 + tx + 16 * j) ? s[i][j] * scale_log2 : -INFINITY;
+                s[i][j] = chunk_sees(u, pos[i], key[j]) ? s[i][j] * scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[i][j]);
             }
 #pragma unroll

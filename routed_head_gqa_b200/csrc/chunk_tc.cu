@@ -134,7 +134,7 @@ __device__ __forceinline__ int tile_steps(const ChunkGeom& u, const ChunkItem& i
     if (few) return (it.s1 - it.s0 + 1 - t) >> 1;
     if (it.nt <= t * u.W) return 0;
     const int hi = it.p0 + min(it.nt, (t + 1) * u.W);
-    const int end = min(it.s1, it.sink_tiles + (hi + kBN - 1) / kBN - it.lo_tile);
+    const int end = min(it.s1, (hi - it.skip + kBN - 1) / kBN);
     return max(0, end - it.s0);
 }
 
@@ -232,8 +232,8 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
         for (int r = 0; r < 16; ++r) asm volatile("" : "+r"(s[r]));
         tc_fence_before();
         warp_arrive(&sm.st_free[t]);
-        const int kv0 = it.tile(it.s0 + 2 * i + t) * kBN, key = kv0 + col;
-        const bool need_mask = kv0 + kBN - 1 > it.p0 || (u.window && kv0 <= it.hi - 1 - u.window && kv0 + kBN > u.sinks);
+        const int x0 = (it.s0 + 2 * i + t) * kBN, key = it.key(x0 + col);
+        const bool need_mask = x0 + it.skip + kBN - 1 > it.p0 || (u.window && x0 + it.skip <= it.hi - 1 - u.window);
         float x[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(s[r]) * p.scale_log2;
@@ -451,18 +451,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             }
             const ChunkItem it = sm.item[slot];
             for (int s = it.s0; s < it.s1; ++s, ++kv_it) {
-                const int st = kv_it & 1, kv0 = it.tile(s) * kBN;
+                const int st = kv_it & 1, x0 = s * kBN;
                 const uint32_t par = ((kv_it >> 1) & 1) ^ 1;
                 int page = 0, in_page = 0, row[4];
                 if constexpr (kGather) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int key = kv0 + lane * 4 + e;
+                        const int key = it.key(x0 + lane * 4 + e);
                         const bool on = key < it.hi && (key >= it.lo || key < u.sinks);
                         row[e] = on ? (int)(chunk_cache_row(u, it.b, key) * u.g + it.q) : p.kv_rows;
                     }
                 } else if (lane < 2 * boxes) {
-                    const int key = kv0 + (lane >> 1) * box_rows;
+                    const int key = it.key(x0 + (lane >> 1) * box_rows);
                     const bool on = key < it.hi && (key + box_rows > it.lo || key < u.sinks);
                     page = u.num_pages;  // outside the pool: zeros
                     in_page = key & ((1 << shift) - 1);
@@ -649,20 +649,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 if (!warp_wait(sm, u, &sm.kv_full_v[kv_it & 1], (kv_it >> 1) & 1, 31)) { ok = false; break; }
                 // Rows of loaded pages that no row of the unit sees: past the last
                 // token, and between the first `sinks` keys and the window.
-                const int kv0 = it.tile(it.s0 + i) * kBN, kv1 = kv0 + kBN;
-                if (kv1 > it.hi || kv0 < it.lo) {
+                const int x0 = (it.s0 + i) * kBN, x1 = x0 + kBN;  // of the key list
+                if (x1 > it.hi - it.skip || (u.window && x0 < it.lo - it.skip)) {
                     uint8_t* v = sm.v[kv_it & 1];
                     auto zero = [&](int a, int b) {
-                        a = max(a, kv0);
-                        b = min(b, kv1);
+                        a = max(a, x0);
+                        b = min(b, x1);
                         for (int x = lane; x < (b - a) * 16; x += 32)
-                            *reinterpret_cast<uint4*>(v + ((x & 8) ? kHalf : 0) + (a - kv0 + (x >> 4)) * 128 + (x & 7) * 16) =
+                            *reinterpret_cast<uint4*>(v + ((x & 8) ? kHalf : 0) + (a - x0 + (x >> 4)) * 128 + (x & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                     };
-                    zero(it.hi, (it.hi + page - 1) & ~(page - 1));
+                    zero(it.hi - it.skip, ((it.hi + page - 1) & ~(page - 1)) - it.skip);
                     if (u.window) {
-                        zero(u.sinks, min(it.lo, (u.sinks + page - 1) & ~(page - 1)));
-                        zero(max(u.sinks, it.lo & ~(page - 1)), it.lo);
+                        zero(u.sinks, it.head);
+                        zero(max(it.head + it.skip, u.sinks) - it.skip, it.lo - it.skip);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -783,8 +783,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 }
                 tc_fence_after();
                 uint32_t s[4][32];
-                const int kv0 = it.tile(it.s0 + i) * kBN;
-                const bool need_mask = kv0 + kBN - 1 > pos_first || (kv0 < low_last && kv0 + kBN > u.sinks);
+                const int x0 = (it.s0 + i) * kBN, kv0 = x0 + it.skip;  // of the key list; its key behind the first ones
+                const bool need_mask = kv0 + kBN - 1 > pos_first || kv0 < low_last;
                 uint64_t sum2[4] = {0, 0, 0, 0};
                 float m_use = m;
                 bool done = false, slot_ok = true;
@@ -845,8 +845,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (need_mask) {
 #pragma unroll
                         for (int cb = 0; cb < 4; ++cb) {
-                            const int k0 = kv0 + cb * 32;
-                            const uint32_t see = low_bits(pos + 1 - k0) & (~low_bits(low < k0 ? 0 : low - k0) | low_bits(u.sinks - k0));
+                            const int k0 = kv0 + cb * 32, head = it.head - x0 - cb * 32;
+                            uint32_t see = low_bits(pos + 1 - k0) & (~low_bits(low < k0 ? 0 : low - k0) | low_bits(u.sinks - k0));
+                            if (head > 0) see = (see & ~low_bits(head)) | low_bits(min(head, u.sinks - x0 - cb * 32));
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (!(see & (1u << e))) s[cb][e] = __float_as_uint(-INFINITY);
