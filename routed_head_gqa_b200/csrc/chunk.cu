@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
 chunk_combine_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
                      float scale_log2, T* __restrict__ O) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kRec = D + 4, kPer = D / 32;
     __shared__ int list[kChunkMaxParts];  // the unit's records in order
     __shared__ int count;
@@ -59,7 +60,7 @@ chunk_combine_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __rest
         if (lane == 0) count = n;
     }
     if (odd) {
-        chunk_split(u, split, cta);
+        chunk_split<32 * kCombineWarps>(u, split, cta);
         ChunkWalk walk(u, split, kind, cta);
         ChunkItem it;
         while (walk.next(u, it, false)) {
@@ -156,6 +157,7 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     u.g = s.g;
     u.k = s.k;
     u.hpg = s.h / s.g;
+    u.inv_k = (65536 + s.k - 1) / s.k;
     u.W = t.rows / s.k;
     u.WU = t.tiles * u.W;
     u.BN = t.keys;

@@ -40,6 +40,7 @@ struct ChunkDesc {
 
 struct ChunkGeom {
     int T, n_seqs, h, g, k, hpg;
+    uint32_t inv_k;   // row / k == row * inv_k >> 16 for a unit's rows
     int W, WU;        // tokens per query tile and per unit
     int BN, bn_shift; // keys per step and their log2
     int align;        // rows that the parts of a unit's key list are aligned to
@@ -107,21 +108,24 @@ __device__ __forceinline__ int chunk_units(const ChunkGeom& u, int n) { return (
 
 // Cost of the first i units of a request and group in closed form: unit j sees
 // about first + j * WU keys, or the window's span if that is less.
-__device__ __forceinline__ uint32_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s, int i) {
-    const uint32_t first = s.L - s.n + min(s.n, u.WU);
-    uint32_t grow = i;
-    uint64_t keys = 0;
-    if (u.window) {
-        const uint32_t span = (uint32_t)u.window + u.WU + u.sinks;  // window and sinks are at most 2^30
-        grow = first < span ? min((uint32_t)i, (span - first + u.WU - 1) / (uint32_t)u.WU) : 0;
-        keys = (uint64_t)(i - grow) * span;
+struct ChunkCost {
+    uint32_t first, span, grow;  // units before `grow` still grow
+    __device__ __forceinline__ ChunkCost(const ChunkGeom& u, const ChunkSeq& s)
+        : first(s.L - s.n + min(s.n, u.WU)), span(0), grow(0xffffffffu) {
+        if (u.window) {
+            span = (uint32_t)u.window + u.WU + u.sinks;  // window and sinks are at most 2^30
+            grow = first < span ? (span - first + u.WU - 1) / (uint32_t)u.WU : 0;
+        }
     }
-    keys += (uint64_t)grow * first;
-    if (grow > 1) keys += (uint64_t)u.WU * ((uint64_t)grow * (grow - 1) / 2);
-    return (uint32_t)(keys >> u.cost_shift) + i * u.unit_cost;
-}
+    __device__ __forceinline__ uint32_t operator()(const ChunkGeom& u, uint32_t i) const {
+        const uint32_t n = min(i, grow);
+        uint64_t keys = (uint64_t)n * first + (uint64_t)(i - n) * span;
+        if (n > 1) keys += (uint64_t)u.WU * ((uint64_t)n * (n - 1) / 2);
+        return (uint32_t)(keys >> u.cost_shift) + i * u.unit_cost;
+    }
+};
 __device__ __forceinline__ uint32_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s) {
-    return s.n > 0 ? u.g * chunk_cost(u, s, chunk_units(u, s.n)) : 0;
+    return s.n > 0 ? u.g * ChunkCost(u, s)(u, chunk_units(u, s.n)) : 0;
 }
 
 __device__ __forceinline__ void chunk_item(const ChunkGeom& u, const ChunkSeq& s, int b, int q, int i, ChunkItem& it) {
@@ -155,40 +159,45 @@ struct ChunkPlace {
     int b, q, i, s;
 };
 
-// Where a cost `rest` (within request b's own cost) falls.  The quotients are
-// taken in fp32: they only place the boundaries, and the two parts that meet at
-// one evaluate the same expression.
+// Where a cost `rest` (within request b's own cost) falls (warp-collective, the same
+// in every lane).  The quotients are taken in fp32: they only place the
+// boundaries, and the two parts that meet at one evaluate the same expression.
 __device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const ChunkSeq& s, int b, uint32_t rest) {
-    const int units = chunk_units(u, s.n);
-    const uint32_t per = chunk_cost(u, s, units);
+    const int units = chunk_units(u, s.n), lane = threadIdx.x & 31;
+    const ChunkCost cost(u, s);
+    const uint32_t per = cost(u, units);
     ChunkPlace pl;
     pl.b = b;
     pl.q = min((int)__fdividef((float)rest, (float)per), u.g - 1);
     if (rest < pl.q * per) --pl.q;
     if (pl.q + 1 < u.g && rest >= (pl.q + 1) * per) ++pl.q;
     rest -= pl.q * per;
-    int lo = 0;
-    uint32_t before = 0, cost = per;
-    if (units > 1) {
-        int hi = units - 1;  // the last unit whose prefix does not exceed rest
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (chunk_cost(u, s, mid) <= rest) lo = mid; else hi = mid - 1;
-        }
-        before = chunk_cost(u, s, lo);
-        cost = chunk_cost(u, s, lo + 1) - before;
+    // the last unit whose prefix does not exceed rest: 32 candidates a round
+    int lo = 0, span = units;
+    while (span > 1) {
+        const int step = (span + 31) >> 5, at = lo + lane * step;
+        const unsigned under = __ballot_sync(0xffffffffu, at < lo + span && cost(u, at) <= rest);
+        const int hit = 31 - __clz(under);  // lane 0 always is
+        span = min(step, span - hit * step);
+        lo += hit * step;
     }
+    const uint32_t before = units > 1 ? cost(u, lo) : 0, own = units > 1 ? cost(u, lo + 1) - before : per;
     pl.i = lo;
     ChunkItem it;
     chunk_item(u, s, b, pl.q, lo, it);
-    pl.s = max(0, min((int)(__fdividef((float)(rest - before), (float)cost) * it.steps), it.steps - 1));
+    pl.s = max(0, min((int)(__fdividef((float)(rest - before), (float)own) * it.steps), it.steps - 1));
     return pl;
 }
 
-// Shared state of the split: filled by chunk_split, read by the item walk.
+// Shared state of the split: filled by chunk_split, read by the item walk.  An end
+// is a request and a cost within it; request n_seqs: none.
+struct ChunkEnd {
+    int b;
+    uint32_t rest;
+};
 struct ChunkSplit {
     uint32_t warp_sum[2][32];
-    ChunkPlace from[2], to[2];  // by kind
+    ChunkEnd end[2][2];  // by kind: this CTA's first place, and the first that is no longer its own
 };
 
 // The part that a CTA takes of a kind: opposite ends, so that small amounts of
@@ -196,10 +205,12 @@ struct ChunkSplit {
 __device__ __forceinline__ int chunk_part(const ChunkGeom& u, int kind, int cta) { return kind ? cta : u.parts - 1 - cta; }
 
 // A CTA's first place and the first place that is no longer its own, of each
-// kind.  Called by all threads of a block (at most 1024, whole warps).
+// kind.  Called by all kThreads threads of a block.
+template <int kThreads>
 __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, int cta) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    const int per = (u.n_seqs + blockDim.x - 1) / blockDim.x;
+    constexpr int nw = kThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = u.n_seqs <= kThreads ? 1 : (u.n_seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, u.n_seqs), b1 = min(b0 + per, u.n_seqs);
     ChunkSeq only;  // the request of a thread that has one
     uint32_t mine[2] = {0, 0};
@@ -208,10 +219,7 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
         const uint32_t cost = chunk_cost(u, only);
         if (chunk_kind(u, only.n)) mine[1] += cost; else mine[0] += cost;
     }
-    if (tid < 2) {  // overwritten below where the place exists
-        sp.from[tid] = {u.n_seqs, 0, 0, 0};
-        sp.to[tid] = {u.n_seqs, 0, 0, 0};
-    }
+    if (tid < 4) sp.end[tid >> 1][tid & 1] = {u.n_seqs, 0};  // overwritten below where the place exists
     uint32_t run[2] = {mine[0], mine[1]};
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -231,6 +239,7 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
         const uint32_t own = kind ? mine[1] : mine[0];
         if (own == 0) continue;
         uint32_t before = (kind ? run[1] : run[0]) - own, total = 0;
+#pragma unroll
         for (int w = 0; w < nw; ++w) {
             if (w < warp) before += sp.warp_sum[kind][w];
             total += sp.warp_sum[kind][w];
@@ -249,8 +258,7 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
                 const ChunkSeq s = per == 1 ? only : chunk_seq(u, b);
                 const uint32_t cost = chunk_kind(u, s.n) == kind ? chunk_cost(u, s) : 0;
                 if (x - at < cost) {
-                    const ChunkPlace pl = chunk_place(u, s, b, x - at);
-                    if (e) sp.to[kind] = pl; else sp.from[kind] = pl;
+                    sp.end[kind][e] = {b, x - at};
                     break;
                 }
                 at += cost;
@@ -267,7 +275,12 @@ struct ChunkWalk {
     ChunkSeq held;       // request base + lane
     int kind, base, part;
     __device__ __forceinline__ ChunkWalk(const ChunkGeom& u, const ChunkSplit& sp, int kind, int cta)
-        : at(sp.from[kind]), to(sp.to[kind]), kind(kind), base(-64), part(chunk_part(u, kind, cta)) {}
+        : kind(kind), base(-64), part(chunk_part(u, kind, cta)) {
+        const ChunkEnd e0 = sp.end[kind][0], e1 = sp.end[kind][1];
+        at = to = {u.n_seqs, 0, 0, 0};
+        if (e0.b < u.n_seqs) at = chunk_place(u, chunk_seq(u, e0.b), e0.b, e0.rest);
+        if (e1.b < u.n_seqs) to = chunk_place(u, chunk_seq(u, e1.b), e1.b, e1.rest);
+    }
     // describe: write the descriptors of split units
     __device__ __forceinline__ bool next(const ChunkGeom& u, ChunkItem& it, bool describe = true) {
         const int lane = threadIdx.x & 31;
@@ -309,8 +322,13 @@ struct ChunkWalk {
     }
 };
 
-// Marks this CTA's descriptors and flags unused, before its walks (by the lane 0
-// that writes the descriptors).
+// Whether a CTA has items of a kind.
+__device__ __forceinline__ bool chunk_has(const ChunkGeom& u, const ChunkSplit& sp, int kind) {
+    return sp.end[kind][0].b < u.n_seqs;
+}
+
+// Marks this CTA's descriptors and flags unused (one thread, a block barrier
+// before the walks).
 __device__ __forceinline__ void chunk_clear(const ChunkGeom& u) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)

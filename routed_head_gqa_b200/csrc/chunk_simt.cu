@@ -275,8 +275,9 @@ chunk_simt_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restric
     T* Vs = Ks + kBN * C::kKV;
     const int tid = threadIdx.x;
 
-    chunk_split(u, sh.split, blockIdx.x);
     if (tid == 0) chunk_clear(u);
+    chunk_split<kThreads>(u, sh.split, blockIdx.x);
+    if (!chunk_has(u, sh.split, 0)) return;
     ChunkWalk walk(u, sh.split, 0, blockIdx.x);
     while (true) {
         if (tid < 32) {

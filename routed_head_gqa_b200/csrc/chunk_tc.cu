@@ -67,21 +67,35 @@ struct Smem {
     uint8_t v[2][kTileBytes];
     uint8_t p[kQT][kFew * 256];          // few rows: P_t [16 rows][128 keys] bf16, two 64-key halves
     float x[kFew][kD];                   // few rows: O^T_1 on its way to warpgroup 0
+    // Many rows: 64 bytes of each of a softmax warp's 32 rows on their way out, in a
+    // half of the group's own p and of x.
+    __device__ __forceinline__ uint4* stage(int t, int w) {
+        return reinterpret_cast<uint4*>(w < 2 ? p[t] + w * 2048 : reinterpret_cast<uint8_t*>(x) + t * 4096 + (w - 2) * 2048);
+    }
     float x_ml[2][kFew];                 //   with its maxima and sums
+    uint4 zero[kD * 2 / 16];             // a row of zeros, for the unselected output slots
     float4 wmax[kQT][2][kFew];           // few rows: the four warps' maxima of a step
     float4 wsum[kQT][kFew];              //   and their sums at the end
     ChunkItem item[kItems];
     int32_t has[kItems];                 // 0: no more items of the kind
     int32_t row_j[kItems][kQT][kBM];     // head of each query row, -1: none
     ChunkSplit split;
-    uint64_t item_full[kItems], item_free[kItems], rows_full[kItems];
+    // barriers, in the order of kBarCounts
+    uint64_t item_full[kItems], rows_full[kItems], item_free[kItems];
     uint64_t kv_full_k[2], kv_full_v[2], kv_empty_k[2], kv_empty_v[2];
-    uint64_t s_full[kQT], p_full[kQT], p_empty[kQT], o_full[kQT], o_empty[kQT];
-    uint64_t st_free[kQT], vote[kQT], x_full, x_free;
-    uint64_t s_free, q_full, q_empty, mma_drain, mma_drain2;
+    uint64_t s_full[kQT], p_empty[kQT], o_full[kQT], q_full[kQT], q_empty[kQT], p_full[kQT], o_empty[kQT], st_free[kQT], vote[kQT];
+    uint64_t x_full, x_free, s_free, mma_drain, mma_drain2;
     uint32_t tmem_base;
     int32_t abort_flag;
 };
+
+// Arrivals that complete a barrier: 11 readers of an item (warps 0, 1, 3 and the
+// eight softmax warps), the four warps of a warpgroup, or one.
+__device__ __forceinline__ uint32_t bar_count(int i) {
+    constexpr int kFree = 2 * kItems, kOnes = 3 * kItems, kWarps = kOnes + 8 + 5 * kQT, kTail = kWarps + 4 * kQT + 3;
+    return i < kFree ? 1 : i < kOnes ? 11 : i < kWarps ? 1 : i < kTail ? 4 : 1;
+}
+constexpr int kBars = 3 * kItems + 8 + 9 * kQT + 5;
 
 struct Params {
     bf16* O;
@@ -138,13 +152,12 @@ __device__ __forceinline__ int tile_steps(const ChunkGeom& u, const ChunkItem& i
     return max(0, end - it.s0);
 }
 
-// The kinds of units in the order in which this CTA runs them: every other CTA
-// begins with the few-row units, whose K/V stream from HBM while the others keep
-// the tensor cores busy.
-__device__ __forceinline__ int first_kind() { return blockIdx.x & 1; }
-
 // Bits 0 .. n-1 of a word (n clamped to 0 .. 32).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    uint32_t m;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(max(n, 0)));
+    return m;
+}
 
 // S_t = Q_t K(it)^T: eight K steps of 16 over 128-byte swizzled tiles; a step
 // moves the descriptors' start address only.
@@ -208,7 +221,10 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
     const bool partial = it.rec >= 0;
     // gate of row `lane`, in flight until the epilogue
     float gate = 0.f;
-    if (t == 0 && !partial && lane < rows) gate = u.gate[((int64_t)(it.t0 + lane / u.k) * u.g + it.q) * u.k + lane % u.k];
+    if (t == 0 && !partial && lane < rows) {
+        const int token = lane * u.inv_k >> 16;
+        gate = u.gate[((int64_t)(it.t0 + token) * u.g + it.q) * u.k + lane - token * u.k];
+    }
     float m[NR], l[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -367,7 +383,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
             rec[col] = none ? 0.f : v / l[r];
             if (col == 0) rec[kD] = none ? -INFINITY : m[r] + log2f(l[r]);
         } else {
-            p.O[((int64_t)(it.t0 + r / u.k) * u.h + head) * kD + col] = __float2bfloat16_rn(v * (gm / l[r]));
+            p.O[((int64_t)(it.t0 + (r * u.inv_k >> 16)) * u.h + head) * kD + col] = __float2bfloat16_rn(v * (gm / l[r]));
         }
     }
     if (!(check == 0.f) && !partial) u.odd[u.parts + blockIdx.x] = 1;
@@ -383,38 +399,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     Smem& sm = *smem_align1024<Smem>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.kv_full_k[i], 1);
-            mbar_init(&sm.kv_full_v[i], 1);
-            mbar_init(&sm.kv_empty_k[i], 1);
-            mbar_init(&sm.kv_empty_v[i], 1);
-        }
-        for (int i = 0; i < kItems; ++i) {
-            mbar_init(&sm.item_full[i], 1);
-            mbar_init(&sm.rows_full[i], 1);
-            mbar_init(&sm.item_free[i], 11);  // warps 0, 1, 3 and the eight softmax warps
-        }
-        for (int t = 0; t < kQT; ++t) {
-            mbar_init(&sm.s_full[t], 1);
-            mbar_init(&sm.p_full[t], 4);   // one arrive per warp of the tile's warpgroup
-            mbar_init(&sm.p_empty[t], 1);
-            mbar_init(&sm.o_full[t], 1);
-            mbar_init(&sm.o_empty[t], 4);
-        }
-        for (int t = 0; t < kQT; ++t) {
-            mbar_init(&sm.st_free[t], 4);
-            mbar_init(&sm.vote[t], 4);
-        }
-        mbar_init(&sm.x_full, 4);
-        mbar_init(&sm.x_free, 4);
-        mbar_init(&sm.s_free, 4);
-        mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.q_empty, 1);
-        mbar_init(&sm.mma_drain, 1);
-        mbar_init(&sm.mma_drain2, 1);
-        sm.abort_flag = 0;
+    static_assert(kBars <= 64, "one barrier per thread of warps 1 and 2");
+    if (warp == 1 || warp == 2) {
+        if (tid - 32 < kBars) mbar_init(&sm.item_full[0] + (tid - 32), bar_count(tid - 32));
         fence_barrier_init();
+    }
+    if (tid == 96) sm.abort_flag = 0;
+    if (warp == 4 && lane < kD * 2 / 16) {
+        sm.zero[lane] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
     }
     if (warp == 0) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -423,10 +416,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     // Launched as a programmatic dependent of the kernel before it: the set-up
     // above overlaps its tail; nothing it writes is read before this wait.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Blocks of the merge may take their places as this kernel's leave.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 96) chunk_clear(u);
     tc_fence_before();
-    chunk_split(u, sm.split, blockIdx.x);  // with block barriers
+    chunk_split<kThreads>(u, sm.split, blockIdx.x);  // with block barriers
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    // The kinds of units this CTA has, in the order in which it runs them: every
+    // other CTA begins with the few-row ones, whose K/V stream from HBM while the
+    // others keep the tensor cores busy.
+    const bool has_many = chunk_has(u, sm.split, 0), has_few = chunk_has(u, sm.split, 1);
+    if (!has_many && !has_few) {
+        if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
+    const int phases = has_many && has_few ? 2 : 1;
+    const bool few_first = has_few && (!has_many || (blockIdx.x & 1));
 
     if (warp == 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
@@ -441,12 +447,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             tma_prefetch_desc(&mapK);
             tma_prefetch_desc(&mapV);
         }
-        for (uint32_t ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
+        for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
             const int slot = ui % kItems;
             if (!warp_wait(sm, u, &sm.item_full[slot], (ui / kItems) & 1, 1)) break;
             if (!sm.has[slot]) {
                 warp_arrive(&sm.item_free[slot]);
-                if (++ends == 2) break;
+                if (++ends == phases) break;
                 continue;
             }
             const ChunkItem it = sm.item[slot];
@@ -509,21 +515,30 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             // the S buffer is free: its last reader of either form is done
             auto s_buffer = [&]() { return s_cnt == 0 || mbar_wait(&sm.s_free, (s_cnt - 1) & 1); };
             auto st_buffer = [&](int t) { return st_cnt[t] == 0 || mbar_wait(&sm.st_free[t], (st_cnt[t] - 1) & 1); };
-            bool few = first_kind() == 1;
-            uint32_t q_it = 0;
-            for (uint32_t ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
+            bool few = few_first;
+            uint32_t q_use[kQT] = {0, 0}, few_it = 0;  // fills of the Q buffers so far; few-row items
+            for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
                 const int slot = ui % kItems;
                 if (!mbar_wait(&sm.item_full[slot], (ui / kItems) & 1)) { fail(sm, u, 10); break; }
                 if (!sm.has[slot]) {
                     mbar_arrive(&sm.item_free[slot]);
-                    if (++ends == 2) break;
+                    if (++ends == phases) break;
                     few = !few;
                     continue;
                 }
                 const int n = sm.item[slot].s1 - sm.item[slot].s0;
                 const int n0 = tile_steps(u, sm.item[slot], 0, few), n1 = tile_steps(u, sm.item[slot], 1, few);
+                const int tiles = sm.item[slot].nt > u.W ? 2 : 1;
                 mbar_arrive(&sm.item_free[slot]);
-                if (!mbar_wait(&sm.q_full, q_it++ & 1)) { fail(sm, u, 11); break; }
+                // Q: few rows, the buffers in turn; many, one per tile
+                const int qb = few ? few_it++ & 1 : 0;
+                const uint32_t q_lo = qb ? q_lo1 : q_lo0;
+                for (int t = 0; t < kQT && ok; ++t) {
+                    if (few ? t != qb : t > 0 && tiles < 2) continue;
+                    ok = mbar_wait(&sm.q_full[t], (t ? q_use[1] : q_use[0]) & 1);
+                    if (t) ++q_use[1]; else ++q_use[0];
+                }
+                if (!ok) { fail(sm, u, 11); break; }
                 if (few ? !s_buffer() : !(st_buffer(0) && st_buffer(1))) { fail(sm, u, 14); break; }
                 for (int i = 0; i < n && ok; ++i, ++kv_it) {
                     if (!mbar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1)) { fail(sm, u, 12); ok = false; break; }
@@ -531,7 +546,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         const int t = i & 1;
                         if (!st_buffer(t)) { fail(sm, u, 15); ok = false; break; }
                         tc_fence_after();
-                        issue_st(tmem, dhi, t, q_lo0, (kv_it & 1) ? k_lo1 : k_lo0);
+                        issue_st(tmem, dhi, t, q_lo, (kv_it & 1) ? k_lo1 : k_lo0);
                         umma_commit(&sm.s_full[t]);
                         if (t) ++st_cnt[1]; else ++st_cnt[0];
                     }
@@ -546,7 +561,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (!ok) break;
                     umma_commit(&sm.kv_empty_k[kv_it & 1]);
                 }
-                if (ok) umma_commit(&sm.q_empty);
+                if (!ok) break;
+                if (qb == 0) umma_commit(&sm.q_empty[0]);
+                if (few ? qb == 1 : tiles == 2) umma_commit(&sm.q_empty[1]);
             }
             umma_commit(&sm.mma_drain);  // all issued MMAs complete before TMEM is released
             mbar_wait(&sm.mma_drain, 0);
@@ -556,73 +573,89 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         // ------------------------------------------------------------ items, row tables, Q
         if (lane == 0) {
             tma_prefetch_desc(&mapQ);
-            chunk_clear(u);
         }
-        __syncwarp();
         // this lane's rows 4 lane .. 4 lane + 3 of a tile: token within the tile
         // (negative: none), selection
         int tok[4], sel[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = lane * 4 + e;
-            tok[e] = r < u.W * u.k ? r / u.k : INT_MIN / 2;
-            sel[e] = r % u.k;
+            const int token = r * u.inv_k >> 16;
+            tok[e] = r < u.W * u.k ? token : INT_MIN / 2;
+            sel[e] = r - token * u.k;
         }
-        uint32_t ui = 0, q_it = 0;
+        uint32_t ui = 0, few_it = 0, q_fill[kQT] = {0, 0};
         bool ok = true;
 #pragma unroll 1
-        for (int phase = 0; phase < 2 && ok; ++phase) {
-        const bool few = (phase ^ first_kind()) == 1;
-        ChunkWalk walk(u, sm.split, few, blockIdx.x);
-        for (; !aborted(sm); ++ui) {
-            const int slot = ui % kItems;
-            if (!warp_wait(sm, u, &sm.item_free[slot], ((ui / kItems) & 1) ^ 1, 20)) { ok = false; break; }
-            ChunkItem it;
-            const bool has = walk.next(u, it);  // the same in every lane
-            if (lane == 0) {
-                sm.has[slot] = has;
-                if (has) sm.item[slot] = it;
-                mbar_arrive(&sm.item_full[slot]);
-            }
-            if (!has) {  // every barrier of the ring sees every entry
+        for (int phase = 0; phase < phases && ok; ++phase) {
+            const bool few = (phase == 0) == few_first;
+            ChunkWalk walk(u, sm.split, few, blockIdx.x);
+            for (; !aborted(sm); ++ui) {
+                const int slot = ui % kItems;
+                if (!warp_wait(sm, u, &sm.item_free[slot], ((ui / kItems) & 1) ^ 1, 20)) { ok = false; break; }
+                ChunkItem it;
+                const bool has = walk.next(u, it);  // the same in every lane
+                if (!has) {  // every barrier of the ring sees every entry
+                    if (lane == 0) {
+                        sm.has[slot] = 0;
+                        mbar_arrive(&sm.item_full[slot]);
+                        mbar_arrive(&sm.rows_full[slot]);
+                    }
+                    ++ui;
+                    break;
+                }
+                const int tiles = it.nt > u.W ? 2 : 1, qb = few ? few_it++ & 1 : 0;
+                int row[kQT][4];  // the lane's rows of Q
+#pragma unroll
+                for (int t = 0; t < kQT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int off = tok[e] + t * u.W;
+                        row[t][e] = off >= 0 && off < it.nt ? u.idx[((int64_t)(it.t0 + off) * u.g + it.q) * u.k + sel[e]] : -1;
+                    }
+                auto publish = [&]() {
+                    if (lane == 0) {
+                        sm.has[slot] = 1;
+                        sm.item[slot] = it;
+                        mbar_arrive(&sm.item_full[slot]);
+                    }
+                    __syncwarp();
+                };
+                // The first item's K/V loads queue up behind its Q rows, not before
+                // them; later ones need not wait for the Q buffers to be free.
+                if (ui > 0) publish();
+#pragma unroll
+                for (int t = 0; t < kQT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int off = tok[e] + t * u.W, j = row[t][e];
+                        const bool there = off >= 0 && off < it.nt, good = there && j >= it.q * u.hpg && j < (it.q + 1) * u.hpg;
+                        if (there && !good) report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)(it.t0 + off));
+                        sm.row_j[slot][t][lane * 4 + e] = good ? j : -1;
+                        row[t][e] = good ? (it.t0 + off) * u.h + j : p.q_rows;  // outside: zeros
+                    }
                 warp_arrive(&sm.rows_full[slot]);
-                ++ui;
-                break;
+#pragma unroll
+                for (int t = 0; t < kQT; ++t) {
+                    const int buf = few ? qb : t;
+                    if (t >= tiles) continue;
+                    if (!warp_wait(sm, u, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
+                    if (buf) ++q_fill[1]; else ++q_fill[0];
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[buf], few ? kFew * kD * 2 : kTileBytes);
+                    __syncwarp();
+                    if (!few || lane < kFew / 4) {
+                        uint8_t* dst = sm.q[buf] + lane * 512;
+                        tma_gather4_2d(&mapQ, &sm.q_full[buf], dst, 0, row[t][0], row[t][1], row[t][2], row[t][3]);
+                        tma_gather4_2d(&mapQ, &sm.q_full[buf], dst + kHalf, 64, row[t][0], row[t][1], row[t][2], row[t][3]);
+                    }
+                }
+                if (!ok) break;
+                if (ui == 0) publish();
             }
-            const int tiles = it.nt > u.W ? 2 : 1;
-            int row[kQT][4];  // the lane's rows of Q
-#pragma unroll
-            for (int t = 0; t < kQT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int off = tok[e] + t * u.W;
-                    row[t][e] = off >= 0 && off < it.nt ? u.idx[((int64_t)(it.t0 + off) * u.g + it.q) * u.k + sel[e]] : -1;
-                }
-#pragma unroll
-            for (int t = 0; t < kQT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int off = tok[e] + t * u.W, j = row[t][e];
-                    const bool there = off >= 0 && off < it.nt, good = there && j >= it.q * u.hpg && j < (it.q + 1) * u.hpg;
-                    if (there && !good) report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)(it.t0 + off));
-                    sm.row_j[slot][t][lane * 4 + e] = good ? j : -1;
-                    row[t][e] = good ? (it.t0 + off) * u.h + j : p.q_rows;  // outside: zeros
-                }
-            warp_arrive(&sm.rows_full[slot]);
-            if (!warp_wait(sm, u, &sm.q_empty, (q_it & 1) ^ 1, 21)) { ok = false; break; }
-            if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, few ? kFew * kD * 2 : tiles * kTileBytes);
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < kQT; ++t)
-                if (t < tiles && (!few || lane < kFew / 4)) {
-                    uint8_t* dst = sm.q[t] + lane * 512;
-                    tma_gather4_2d(&mapQ, &sm.q_full, dst, 0, row[t][0], row[t][1], row[t][2], row[t][3]);
-                    tma_gather4_2d(&mapQ, &sm.q_full, dst + kHalf, 64, row[t][0], row[t][1], row[t][2], row[t][3]);
-                }
-            ++q_it;
         }
-        }
-        if (q_it > 0) mbar_wait(&sm.q_full, (q_it - 1) & 1);  // the last Q loads land before the CTA may exit
+        // the last Q loads land before the CTA may exit
+        for (int t = 0; t < kQT; ++t)
+            if ((t ? q_fill[1] : q_fill[0]) > 0) mbar_wait(&sm.q_full[t], ((t ? q_fill[1] : q_fill[0]) - 1) & 1);
     } else if (warp == 3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: O += P V
@@ -632,13 +665,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const int page = 1 << u.page_shift;
         uint32_t kv_it = 0, c[kQT] = {0, 0}, o_cnt[kQT] = {0, 0};
         bool ok = true;
-        bool few = first_kind() == 1;
-        for (uint32_t ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
+        bool few = few_first;
+        for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
             const int slot = ui % kItems;
             if (!warp_wait(sm, u, &sm.item_full[slot], (ui / kItems) & 1, 30)) break;
             if (!sm.has[slot]) {
                 warp_arrive(&sm.item_free[slot]);
-                if (++ends == 2) break;
+                if (++ends == phases) break;
                 few = !few;
                 continue;
             }
@@ -704,8 +737,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const uint32_t s_addr = tmem + lane_off + kColS;
         const uint32_t p_addr = tmem + lane_off + kColP + 64 * t;
         const uint32_t o_addr = tmem + lane_off + kColO + t * 128;
-        const int off = t * u.W + r / u.k;  // this row's token within the unit, and its selection
-        const int sel = r % u.k;
+        const int off = t * u.W + (r * u.inv_k >> 16);  // this row's token within the unit, and its selection
+        const int sel = r - (r * u.inv_k >> 16) * u.k;
         const bool in_tile = r < u.W * u.k;
         const uint64_t C2 = pk2(p.scale_log2, p.scale_log2);
         uint32_t ctile = 0, o_it = 0, votes = 0, swaps = 0;
@@ -719,22 +752,33 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         };
         auto done = [&]() { warp_arrive(&sm.item_free[ui++ % kItems]); };
         // The unselected output slots of the tile's tokens, by the part that holds
-        // the unit's first step.
+        // the unit's first step: a bulk copy of a row of zeros each, the k threads of
+        // a token taking its slots in turn.
         auto zero_fill = [&](const ChunkItem& it, int toks) {
-            if (it.s0 != 0 || u.k == u.hpg) return;
-            const int32_t* heads = sm.row_j[ui % kItems][t];
-            for (int x = wq * 32 + lane; x < toks * u.hpg * 16; x += 128) {
-                const int j = it.q * u.hpg + (x >> 4) % u.hpg, tok = (x >> 4) / u.hpg;
-                bool chosen = false;
-                for (int a = 0; a < u.k; ++a) chosen |= heads[tok * u.k + a] == j;
-                if (!chosen)
-                    *reinterpret_cast<uint4*>(p.O + ((int64_t)(it.t0 + t * u.W + tok) * u.h + j) * kD + (x & 15) * 8) =
-                        make_uint4(0, 0, 0, 0);
+            if (it.s0 != 0 || u.k == u.hpg || r >= toks * u.k) return;
+            const int32_t* heads = sm.row_j[ui % kItems][t] + (r - sel);
+            bf16* o = p.O + ((int64_t)(it.t0 + off) * u.h + it.q * u.hpg) * kD;
+            int turn = 0;
+            for (int a0 = 0; a0 < u.hpg; a0 += 32) {
+                uint32_t free = low_bits(u.hpg - a0);
+                for (int a = 0; a < u.k; ++a) {
+                    const int j = heads[a] - it.q * u.hpg - a0;
+                    if (j >= 0 && j < 32) free &= ~(1u << j);
+                }
+                for (; free; free &= free - 1) {
+                    if (turn == sel)
+                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                         o + (int64_t)(a0 + __ffs(free) - 1) * kD),
+                                     "r"(smem_u32(sm.zero)), "r"(kD * 2)
+                                     : "memory");
+                    if (++turn == u.k) turn = 0;
+                }
             }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         };
 #pragma unroll 1
-        for (int phase = 0; phase < 2; ++phase) {
-        if ((phase ^ first_kind()) == 1) {
+        for (int phase = 0; phase < phases; ++phase) {
+        if ((phase == 0) == few_first) {
             while (const ChunkItem* next = take()) {
                 const ChunkItem it = *next;
                 const int slot = ui % kItems;
@@ -745,6 +789,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     break;
                 done();
             }
+            // group 0 has read what group 1 handed over: x is the stages' now
+            if (swaps > 0 && !aborted(sm)) warp_wait(sm, u, &sm.x_free, (swaps - 1) & 1, 52);
             continue;
         }
         while (const ChunkItem* next = take()) {
@@ -769,7 +815,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             // Keys this row sees: [low, pos] and those below u.sinks.  A padding row
             // sees all (its result is dropped).
             const int pos = mine ? it.p0 + off : INT_MAX - 1;
-            const int low = mine && u.window ? pos - u.window + 1 : INT_MIN;
+            const int low = mine ? pos - u.window + 1 : 0;
             const int pos_first = it.p0 + t * u.W, low_last = u.window ? pos_first + toks - u.window : INT_MIN;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
@@ -802,11 +848,28 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (ctile > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.p_empty[t], (ctile - 1) & 1))) slot_ok = false;
                     tc_fence_after();
                 };
-                // On an unmasked step after the first, the exponentials are taken
-                // against the running max while the step's row max is formed
-                // alongside: unless some row of the warp grew its max by more than
-                // the threshold, P is final.
-                if (!need_mask && i > 0) {
+                // Hide what a row does not see: per 32 keys a bit each, applied where some
+                // of the warp's rows need it.
+                if (need_mask) {
+#pragma unroll
+                    for (int cb = 0; cb < 4; ++cb) {
+                        const int k0 = kv0 + cb * 32, head = it.head - x0 - cb * 32;
+                        uint32_t see = low_bits(pos + 1 - k0);
+                        if (u.window) {
+                            see &= ~low_bits(low - k0) | low_bits(u.sinks - k0);
+                            if (head > 0) see = (see & ~low_bits(head)) | low_bits(min(head, u.sinks - x0 - cb * 32));
+                        }
+                        if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e))) s[cb][e] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                }
+                // After the first step the exponentials are taken against the running
+                // max while the step's row max is formed alongside: unless some row of
+                // the warp grew its max by more than the threshold, P is final.
+                if (i > 0) {
                     const uint64_t NM2 = pk2(-m, -m);
                     float mq[4];
                     uint32_t pk[4][16];
@@ -842,17 +905,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     }
                 }
                 if (!done) {
-                    if (need_mask) {
-#pragma unroll
-                        for (int cb = 0; cb < 4; ++cb) {
-                            const int k0 = kv0 + cb * 32, head = it.head - x0 - cb * 32;
-                            uint32_t see = low_bits(pos + 1 - k0) & (~low_bits(low < k0 ? 0 : low - k0) | low_bits(u.sinks - k0));
-                            if (head > 0) see = (see & ~low_bits(head)) | low_bits(min(head, u.sinks - x0 - cb * 32));
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see & (1u << e))) s[cb][e] = __float_as_uint(-INFINITY);
-                        }
-                    }
                     float mq[4];
 #pragma unroll
                     for (int cb = 0; cb < 4; ++cb) {
@@ -917,10 +969,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             }
             if (!ok) break;
             // Epilogue: O_t / l, gated, as the bf16 row of O, or the row's partial
-            // record (o, log2-sum-exp); none of this part's keys seen: -inf.
-            float* rec = u.part + (int64_t)(it.rec + t * u.W * u.k + r) * (kD + 4);
+            // record (o, log2-sum-exp); none of this part's keys seen: -inf.  A row per
+            // thread would store 16 bytes to each of 32 lines at a time, so 64 bytes of
+            // each row at a time go through shared memory and out as whole sectors.
+            const int rec_row = it.rec + t * u.W * u.k + wq * 32;
             if (n == 0) {
-                if (partial && mine) rec[kD] = -INFINITY;
+                if (partial && mine) u.part[(int64_t)(rec_row + lane) * (kD + 4) + kD] = -INFINITY;
                 done();
                 continue;
             }
@@ -950,33 +1004,61 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 for (int e = 0; e < 32; ++e) check[e & 3] = fmaf(__uint_as_float(o[cb][e]), 0.f, check[e & 3]);
             if (head >= 0) {
                 if (!partial && !((check[0] + check[1]) + (check[2] + check[3]) == 0.f)) u.odd[blockIdx.x] = 1;
-                if (partial) {
+                if (partial) u.part[(int64_t)(rec_row + lane) * (kD + 4) + kD] = none ? -INFINITY : m + log2f(l);
+            }
+            uint4* stage = sm.stage(t, wq);
+            // Writes 64 bytes of every row of the warp: to[row] + byte offset
+            auto flush = [&](const uint4 (&v)[4], auto address) {
 #pragma unroll
-                    for (int cb = 0; cb < 4; ++cb)
+                for (int c = 0; c < 4; ++c) stage[lane * 4 + (c ^ ((lane >> 1) & 3))] = v[c];
+                __syncwarp();
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            reinterpret_cast<float4*>(rec + cb * 32)[v] =
-                                make_float4(__uint_as_float(o[cb][4 * v]) * f, __uint_as_float(o[cb][4 * v + 1]) * f,
-                                            __uint_as_float(o[cb][4 * v + 2]) * f, __uint_as_float(o[cb][4 * v + 3]) * f);
-                    rec[kD] = none ? -INFINITY : m + log2f(l);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.O + ((int64_t)token * u.h + head) * kD);
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 8 * e + (lane >> 2), c = lane & 3;
+                    uint4* to = address(row, c);
+                    if (to) *to = stage[row * 4 + (c ^ ((row >> 1) & 3))];
+                }
+                __syncwarp();
+            };
+            const int out_row = head >= 0 ? token * u.h + head : -1;
+            if (partial) {
 #pragma unroll
-                    for (int cb = 0; cb < 4; ++cb)
+                for (int cb = 0; cb < 8; ++cb) {
+                    uint4 v[4];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint4 pk;
-                            pk.x = pack_bf16x2(__uint_as_float(o[cb][8 * v + 0]) * f, __uint_as_float(o[cb][8 * v + 1]) * f);
-                            pk.y = pack_bf16x2(__uint_as_float(o[cb][8 * v + 2]) * f, __uint_as_float(o[cb][8 * v + 3]) * f);
-                            pk.z = pack_bf16x2(__uint_as_float(o[cb][8 * v + 4]) * f, __uint_as_float(o[cb][8 * v + 5]) * f);
-                            pk.w = pack_bf16x2(__uint_as_float(o[cb][8 * v + 6]) * f, __uint_as_float(o[cb][8 * v + 7]) * f);
-                            dst[cb * 4 + v] = pk;
-                        }
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t* w = &o[cb >> 1][(cb & 1) * 16 + 4 * c];
+                        v[c] = make_uint4(__float_as_uint(__uint_as_float(w[0]) * f), __float_as_uint(__uint_as_float(w[1]) * f),
+                                          __float_as_uint(__uint_as_float(w[2]) * f), __float_as_uint(__uint_as_float(w[3]) * f));
+                    }
+                    flush(v, [&](int row, int c) -> uint4* {
+                        const int there = __shfl_sync(0xffffffffu, out_row, row);
+                        return there < 0 ? nullptr
+                                         : reinterpret_cast<uint4*>(u.part + (int64_t)(rec_row + row) * (kD + 4) + cb * 16) + c;
+                    });
+                }
+            } else {
+#pragma unroll
+                for (int cb = 0; cb < 4; ++cb) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t* w = &o[cb][8 * c];
+                        v[c].x = pack_bf16x2(__uint_as_float(w[0]) * f, __uint_as_float(w[1]) * f);
+                        v[c].y = pack_bf16x2(__uint_as_float(w[2]) * f, __uint_as_float(w[3]) * f);
+                        v[c].z = pack_bf16x2(__uint_as_float(w[4]) * f, __uint_as_float(w[5]) * f);
+                        v[c].w = pack_bf16x2(__uint_as_float(w[6]) * f, __uint_as_float(w[7]) * f);
+                    }
+                    flush(v, [&](int row, int c) -> uint4* {
+                        const int there = __shfl_sync(0xffffffffu, out_row, row);
+                        return there < 0 ? nullptr : reinterpret_cast<uint4*>(p.O + (int64_t)there * kD + cb * 32) + c;
+                    });
                 }
             }
             done();
         }
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the zero rows are out
     }
 
     __syncwarp();
