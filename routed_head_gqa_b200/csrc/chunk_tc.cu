@@ -57,8 +57,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: p <= 2^8 between rescales
 constexpr uint32_t kWhereChunkTc = 11;     // status "where" id of this kernel
-// Register split (setmaxnreg): 4 control warps at 88, 8 softmax warps at 208.
-constexpr int kRegsLaunch = 168, kRegsCtl = 88, kRegsSoftmax = 208;
+// Register split (setmaxnreg): 4 control warps at 56, 8 softmax warps at 224.
+constexpr int kRegsLaunch = 168, kRegsCtl = 56, kRegsSoftmax = 224;
 static_assert(128 * kRegsCtl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split exceeds the launch");
 
 struct Smem {
@@ -794,7 +794,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             continue;
         }
         while (const ChunkItem* next = take()) {
-            const ChunkItem it = *next;
+            const ChunkItem& it = *next;  // read again where it is used: registers are short in the loop
             const int slot = ui % kItems;
             const int n = tile_steps(u, it, t, false);
             const int toks = min(it.nt - t * u.W, u.W);  // of this tile; 0 or less: none
@@ -819,6 +819,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const int pos_first = it.p0 + t * u.W, low_last = u.window ? pos_first + toks - u.window : INT_MIN;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
+            const int x_first = it.s0 * kBN, skip = it.skip;
             for (int i = 0; i < n; ++i, ++ctile) {
                 if (!warp_wait(sm, u, &sm.s_full[t], ctile & 1, 42)) { ok = false; break; }
                 if (!live) {  // no query row: hand both buffers on, P no sooner than the slot is free
@@ -829,7 +830,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 }
                 tc_fence_after();
                 uint32_t s[4][32];
-                const int x0 = (it.s0 + i) * kBN, kv0 = x0 + it.skip;  // of the key list; its key behind the first ones
+                const int x0 = x_first + i * kBN, kv0 = x0 + skip;  // of the key list; its key behind the first ones
                 const bool need_mask = kv0 + kBN - 1 > pos_first || kv0 < low_last;
                 uint64_t sum2[4] = {0, 0, 0, 0};
                 float m_use = m;
