@@ -32,7 +32,7 @@ chunk_combine_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __rest
                      float scale_log2, T* __restrict__ O) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kRec = D + 4, kPer = D / 32;
+    constexpr int kRec = D + 4, kPer = D / 32, kRows = 4;
     __shared__ int list[kChunkMaxParts];  // the unit's records in order
     __shared__ int count;
     __shared__ ChunkSplit split;
@@ -78,42 +78,64 @@ chunk_combine_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __rest
     if (!d.valid) return;
     __syncthreads();
     const int n = count, rows = d.nt * u.k;
-    for (int r = blockIdx.y * kCombineWarps + warp; r < rows; r += gridDim.y * kCombineWarps) {
-        const int token = d.t0 + r / u.k, slot = r % u.k;
-        const int j = u.idx[((int64_t)token * u.g + d.q) * u.k + slot];
-        const float gate = u.gate[((int64_t)token * u.g + d.q) * u.k + slot];
-        float M = -INFINITY;
-        for (int i = lane; i < n; i += 32) M = fmaxf(M, u.part[(int64_t)(list[i] + r) * kRec + D]);
+    for (int r0 = (blockIdx.y * kCombineWarps + warp) * kRows; r0 < rows; r0 += gridDim.y * kCombineWarps * kRows) {
+        // kRows rows at once, so that their loads are in flight together
+        int j[kRows];
+        float gate[kRows], M[kRows], L[kRows], acc[kRows][kPer];
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        float L = 0.f, acc[kPer];
+        for (int i = 0; i < kRows; ++i) {
+            const int r = min(r0 + i, rows - 1), token = d.t0 + r / u.k;
+            const int64_t at = ((int64_t)token * u.g + d.q) * u.k + r % u.k;
+            j[i] = u.idx[at];
+            gate[i] = u.gate[at];
+            M[i] = -INFINITY;
+            L[i] = 0.f;
+            for (int p = lane; p < n; p += 32) M[i] = fmaxf(M[i], u.part[(int64_t)(list[p] + r) * kRec + D]);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float* rec = u.part + (int64_t)(list[i] + r) * kRec;
-            const float lse = rec[D];
-            if (lse == -INFINITY) continue;  // this part holds no key of the row
-            const float w = fast_exp2(lse - M);
-            L += w;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(rec[e * 32 + lane], w, acc[e]);
+            for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
         }
-        if (j < d.q * u.hpg || j >= (d.q + 1) * u.hpg) continue;  // no such row: its records hold nothing
-        float check = L * 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) check += acc[e] * 0.f;
-        if (__any_sync(0xffffffffu, !(check == 0.f))) {
-            const ChunkSeq s = chunk_seq(u, d.b);
-            ChunkItem it;
-            chunk_item(u, s, d.b, d.q, (d.t0 - s.t0) / u.WU, it);
-            row_again<T, D>(u, it, r, j, Q, Kp, Vp, scale_log2, O);
-            continue;
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], s));
+#pragma unroll 2
+        for (int p = 0; p < n; ++p) {
+            float lse[kRows], v[kRows][kPer];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const float* rec = u.part + (int64_t)(list[p] + min(r0 + i, rows - 1)) * kRec;
+                lse[i] = rec[D];
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) v[i][e] = rec[e * 32 + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (lse[i] == -INFINITY) continue;  // this part holds no key of the row
+                const float w = fast_exp2(lse[i] - M[i]);
+                L[i] += w;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[i][e] = fmaf(v[i][e], w, acc[i][e]);
+            }
         }
-        const float f = gate / L;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            O[((int64_t)token * u.h + j) * D + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i, token = d.t0 + r / u.k;
+            if (r >= rows || j[i] < d.q * u.hpg || j[i] >= (d.q + 1) * u.hpg) continue;  // no such row
+            float check = L[i] * 0.f;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) check += acc[i][e] * 0.f;
+            if (__any_sync(0xffffffffu, !(check == 0.f))) {
+                const ChunkSeq s = chunk_seq(u, d.b);
+                ChunkItem it;
+                chunk_item(u, s, d.b, d.q, (d.t0 - s.t0) / u.WU, it);
+                row_again<T, D>(u, it, r, j[i], Q, Kp, Vp, scale_log2, O);
+                continue;
+            }
+            const float f = gate[i] / L[i];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                O[((int64_t)token * u.h + j[i]) * D + e * 32 + lane] = Elem<T>::from_f(acc[i][e] * f);
+        }
     }
 }
 
@@ -176,12 +198,11 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     // No more than one unit per token, nor than the full ones and one per request.
     int64_t units = (s.T + u.WU - 1) / u.WU + (int64_t)a.n_seqs;
     if (units > s.T) units = s.T;
-    u.cost_shift = 4;
-    while ((units * s.g * ((int64_t)u.cap + u.WU + t.unit_keys) >> u.cost_shift) + units * s.g >= ((int64_t)1 << 31))
-        ++u.cost_shift;
-    u.unit_cost = t.unit_keys >> u.cost_shift > 0 ? t.unit_keys >> u.cost_shift : 1;
-    const int least = t.min_keys >> u.cost_shift;
-    u.per_min = 1.0f / (least > 0 ? least : 1);
+    u.unit_cost = (float)t.unit_keys;
+    u.cost_scale = 1.0f / 16;
+    while ((double)units * s.g * ((double)u.cap + u.WU + t.unit_keys) * u.cost_scale + (double)units * s.g > 2.0e9)
+        u.cost_scale *= 0.5f;
+    u.per_min = 1.0f / (t.min_keys * u.cost_scale);
     u.num_pages = a.num_pages;
     u.max_blocks = a.max_blocks;
     u.cu = a.cu_new;

@@ -44,8 +44,8 @@ struct ChunkGeom {
     int W, WU;        // tokens per query tile and per unit
     int BN, bn_shift; // keys per step and their log2
     int align;        // rows that the parts of a unit's key list are aligned to
-    int cost_shift;   // costs are counted in 2^cost_shift keys, so that a step's total fits 32 bits
-    uint32_t unit_cost;  // a unit's fixed cost
+    float unit_cost;  // a unit's fixed cost, in keys
+    float cost_scale; // requests' costs are summed in whole multiples of 1 / cost_scale keys: 32 bits hold a step's
     float per_min;    // 1 / the smallest cost worth a part
     int few_tokens;   // new tokens up to which a request is of the second kind
     int parts;        // CTAs, and parts of either kind at most
@@ -106,26 +106,27 @@ __device__ __forceinline__ int chunk_kind(const ChunkGeom& u, int n) { return n 
 
 __device__ __forceinline__ int chunk_units(const ChunkGeom& u, int n) { return (n + u.WU - 1) / u.WU; }
 
-// Cost of the first i units of a request and group in closed form: unit j sees
-// about first + j * WU keys, or the window's span if that is less.
+// Cost, in keys, of the first i units of a request and group in closed form: unit j
+// sees about first + j * WU keys, or the window's span if that is less.  fp32, as
+// they only place the boundaries and every CTA evaluates the same expressions on
+// the same numbers; the prefix sums over requests are in whole numbers, whose
+// intervals tile without gaps.
 struct ChunkCost {
-    uint32_t first, span, grow;  // units before `grow` still grow
+    float first, span, grow;  // units before `grow` still grow
     __device__ __forceinline__ ChunkCost(const ChunkGeom& u, const ChunkSeq& s)
-        : first(s.L - s.n + min(s.n, u.WU)), span(0), grow(0xffffffffu) {
+        : first((float)(s.L - s.n + min(s.n, u.WU)) + u.unit_cost), span(0.f), grow(3.4e38f) {
         if (u.window) {
-            span = (uint32_t)u.window + u.WU + u.sinks;  // window and sinks are at most 2^30
-            grow = first < span ? (span - first + u.WU - 1) / (uint32_t)u.WU : 0;
+            span = (float)u.window + (float)(u.WU + u.sinks) + u.unit_cost;
+            grow = ceilf(fmaxf(__fdividef(span - first, (float)u.WU), 0.f));
         }
     }
-    __device__ __forceinline__ uint32_t operator()(const ChunkGeom& u, uint32_t i) const {
-        const uint32_t n = min(i, grow);
-        uint64_t keys = (uint64_t)n * first + (uint64_t)(i - n) * span;
-        if (n > 1) keys += (uint64_t)u.WU * ((uint64_t)n * (n - 1) / 2);
-        return (uint32_t)(keys >> u.cost_shift) + i * u.unit_cost;
+    __device__ __forceinline__ float operator()(const ChunkGeom& u, int units) const {
+        const float i = (float)units, n = fminf(i, grow);
+        return n * (first + 0.5f * u.WU * (n - 1.f)) + (i - n) * span;
     }
 };
 __device__ __forceinline__ uint32_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s) {
-    return s.n > 0 ? u.g * ChunkCost(u, s)(u, chunk_units(u, s.n)) : 0;
+    return s.n > 0 ? max(__float2uint_rn(u.g * ChunkCost(u, s)(u, chunk_units(u, s.n)) * u.cost_scale), 1u) : 0;
 }
 
 __device__ __forceinline__ void chunk_item(const ChunkGeom& u, const ChunkSeq& s, int b, int q, int i, ChunkItem& it) {
@@ -159,41 +160,39 @@ struct ChunkPlace {
     int b, q, i, s;
 };
 
-// Where a cost `rest` (within request b's own cost) falls (warp-collective, the same
-// in every lane).  The quotients are taken in fp32: they only place the
-// boundaries, and the two parts that meet at one evaluate the same expression.
-__device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const ChunkSeq& s, int b, uint32_t rest) {
+// Where a fraction (0 or more, below 1) of request b's work ends (warp-collective,
+// the same in every lane).
+__device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const ChunkSeq& s, int b, float fraction) {
     const int units = chunk_units(u, s.n), lane = threadIdx.x & 31;
     const ChunkCost cost(u, s);
-    const uint32_t per = cost(u, units);
+    const float per = cost(u, units);
     ChunkPlace pl;
     pl.b = b;
-    pl.q = min((int)__fdividef((float)rest, (float)per), u.g - 1);
-    if (rest < pl.q * per) --pl.q;
-    if (pl.q + 1 < u.g && rest >= (pl.q + 1) * per) ++pl.q;
-    rest -= pl.q * per;
+    fraction *= u.g;
+    pl.q = min((int)fraction, u.g - 1);
+    const float rest = (fraction - pl.q) * per;
     // the last unit whose prefix does not exceed rest: 32 candidates a round
     int lo = 0, span = units;
     while (span > 1) {
         const int step = (span + 31) >> 5, at = lo + lane * step;
-        const unsigned under = __ballot_sync(0xffffffffu, at < lo + span && cost(u, at) <= rest);
-        const int hit = 31 - __clz(under);  // lane 0 always is
+        const unsigned under = __ballot_sync(0xffffffffu, at < lo + span && cost(u, at) <= rest) | 1u;
+        const int hit = 31 - __clz(under);
         span = min(step, span - hit * step);
         lo += hit * step;
     }
-    const uint32_t before = units > 1 ? cost(u, lo) : 0, own = units > 1 ? cost(u, lo + 1) - before : per;
     pl.i = lo;
+    const float before = cost(u, lo), own = cost(u, lo + 1) - before;
     ChunkItem it;
     chunk_item(u, s, b, pl.q, lo, it);
-    pl.s = max(0, min((int)(__fdividef((float)(rest - before), (float)own) * it.steps), it.steps - 1));
+    pl.s = max(0, min((int)(__fdividef(rest - before, own) * it.steps), it.steps - 1));
     return pl;
 }
 
 // Shared state of the split: filled by chunk_split, read by the item walk.  An end
-// is a request and a cost within it; request n_seqs: none.
+// is a request and a fraction of its work; request n_seqs: none.
 struct ChunkEnd {
     int b;
-    uint32_t rest;
+    float fraction;
 };
 struct ChunkSplit {
     uint32_t warp_sum[2][32];
@@ -212,14 +211,13 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = u.n_seqs <= kThreads ? 1 : (u.n_seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, u.n_seqs), b1 = min(b0 + per, u.n_seqs);
-    ChunkSeq only;  // the request of a thread that has one
     uint32_t mine[2] = {0, 0};
     for (int b = b0; b < b1; ++b) {
-        only = chunk_seq(u, b);
-        const uint32_t cost = chunk_cost(u, only);
-        if (chunk_kind(u, only.n)) mine[1] += cost; else mine[0] += cost;
+        const ChunkSeq s = chunk_seq(u, b);
+        const uint32_t cost = chunk_cost(u, s);
+        if (chunk_kind(u, s.n)) mine[1] += cost; else mine[0] += cost;
     }
-    if (tid < 4) sp.end[tid >> 1][tid & 1] = {u.n_seqs, 0};  // overwritten below where the place exists
+    if (tid < 4) sp.end[tid >> 1][tid & 1] = {u.n_seqs, 0.f};  // overwritten below where the place exists
     uint32_t run[2] = {mine[0], mine[1]};
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -247,18 +245,16 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
         const float want = (float)total * u.per_min;
         const int parts = want < 1.f ? 1 : want > (float)u.parts ? u.parts : (int)want;
         const int c = chunk_part(u, kind, cta);
-        if (c >= parts) continue;
 #pragma unroll 1
         for (int e = 0; e < 2 && c + e < parts; ++e) {  // the last part ends with the step
-            const uint32_t frac = (uint32_t)(__fdiv_rn((float)(c + e), (float)parts) * 4294967296.f);
-            const uint32_t x = __umulhi(total, frac);  // total * (c + e) / parts
+            const uint32_t x = __umulhi(total, (uint32_t)(__fdividef((float)(c + e), (float)parts) * 4294967296.f));
             if (x < before || x - before >= own) continue;
             uint32_t at = before;
             for (int b = b0; b < b1; ++b) {
-                const ChunkSeq s = per == 1 ? only : chunk_seq(u, b);
+                const ChunkSeq s = chunk_seq(u, b);
                 const uint32_t cost = chunk_kind(u, s.n) == kind ? chunk_cost(u, s) : 0;
                 if (x - at < cost) {
-                    sp.end[kind][e] = {b, x - at};
+                    sp.end[kind][e] = {b, __fdividef((float)(x - at), (float)cost)};
                     break;
                 }
                 at += cost;
@@ -276,10 +272,13 @@ struct ChunkWalk {
     int kind, base, part;
     __device__ __forceinline__ ChunkWalk(const ChunkGeom& u, const ChunkSplit& sp, int kind, int cta)
         : kind(kind), base(-64), part(chunk_part(u, kind, cta)) {
-        const ChunkEnd e0 = sp.end[kind][0], e1 = sp.end[kind][1];
-        at = to = {u.n_seqs, 0, 0, 0};
-        if (e0.b < u.n_seqs) at = chunk_place(u, chunk_seq(u, e0.b), e0.b, e0.rest);
-        if (e1.b < u.n_seqs) to = chunk_place(u, chunk_seq(u, e1.b), e1.b, e1.rest);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            const ChunkEnd e = sp.end[kind][i];
+            at = to;
+            to = {u.n_seqs, 0, 0, 0};
+            if (e.b < u.n_seqs) to = chunk_place(u, chunk_seq(u, e.b), e.b, e.fraction);
+        }
     }
     // describe: write the descriptors of split units
     __device__ __forceinline__ bool next(const ChunkGeom& u, ChunkItem& it, bool describe = true) {

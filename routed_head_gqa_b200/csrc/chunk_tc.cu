@@ -18,6 +18,8 @@
 //               from outside the pool, which the TMA fills with zeros.
 //   warp 1      MMA issuer (one thread): S_t = Q_t K^T
 //   warp 2      walks the part's items (a ring of 4), gathers the routed rows of Q
+//               (16-byte asynchronous copies, two whole rows an instruction: gathered
+//               by the TMA four rows at a time, a unit's 256 rows took 9600 clocks)
 //   warp 3      MMA issuer (one thread): O_t += P_t V.  Before it, the whole warp
 //               zeroes the tile's V rows that no row of the unit sees (past the
 //               last token, outside the window): their weight is 0, but 0 times
@@ -57,8 +59,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: p <= 2^8 between rescales
 constexpr uint32_t kWhereChunkTc = 11;     // status "where" id of this kernel
-// Register split (setmaxnreg): 4 control warps at 56, 8 softmax warps at 224.
-constexpr int kRegsLaunch = 168, kRegsCtl = 56, kRegsSoftmax = 224;
+// Register split (setmaxnreg): 4 control warps at 72, 8 softmax warps at 216.
+constexpr int kRegsLaunch = 168, kRegsCtl = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsCtl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split exceeds the launch");
 
 struct Smem {
@@ -98,9 +100,9 @@ __device__ __forceinline__ uint32_t bar_count(int i) {
 constexpr int kBars = 3 * kItems + 8 + 9 * kQT + 5;
 
 struct Params {
+    const bf16* Q;
     bf16* O;
     float scale_log2;
-    int q_rows;   // rows of Q seen as [T * h, 128]
     int kv_rows;  // rows of K seen as [num_pages * page_size * g, 128] (gathered pages only)
 };
 
@@ -394,7 +396,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
 template <bool kGather>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ ChunkGeom u, const Params p) {
+                const __grid_constant__ ChunkGeom u, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     Smem& sm = *smem_align1024<Smem>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -571,9 +573,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     } else if (warp == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         // ------------------------------------------------------------ items, row tables, Q
-        if (lane == 0) {
-            tma_prefetch_desc(&mapQ);
-        }
         // this lane's rows 4 lane .. 4 lane + 3 of a tile: token within the tile
         // (negative: none), selection
         int tok[4], sel[4];
@@ -632,7 +631,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         const bool there = off >= 0 && off < it.nt, good = there && j >= it.q * u.hpg && j < (it.q + 1) * u.hpg;
                         if (there && !good) report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)(it.t0 + off));
                         sm.row_j[slot][t][lane * 4 + e] = good ? j : -1;
-                        row[t][e] = good ? (it.t0 + off) * u.h + j : p.q_rows;  // outside: zeros
+                        row[t][e] = good ? (it.t0 + off) * u.h + j : -1;  // -1: zeros
                     }
                 warp_arrive(&sm.rows_full[slot]);
 #pragma unroll
@@ -641,21 +640,36 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (t >= tiles) continue;
                     if (!warp_wait(sm, u, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
                     if (buf) ++q_fill[1]; else ++q_fill[0];
-                    if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[buf], few ? kFew * kD * 2 : kTileBytes);
-                    __syncwarp();
-                    if (!few || lane < kFew / 4) {
-                        uint8_t* dst = sm.q[buf] + lane * 512;
-                        tma_gather4_2d(&mapQ, &sm.q_full[buf], dst, 0, row[t][0], row[t][1], row[t][2], row[t][3]);
-                        tma_gather4_2d(&mapQ, &sm.q_full[buf], dst + kHalf, 64, row[t][0], row[t][1], row[t][2], row[t][3]);
+                    // Copy j moves rows 2 j and 2 j + 1, half a warp each, to the 128-byte
+                    // swizzled tile; lane r / 4 holds row r.
+                    const int half = lane >> 4, c = lane & 15, copies = few ? kFew / 2 : kBM / 2;
+                    const uint32_t dst = smem_u32(sm.q[buf]) + (c >> 3) * kHalf;
+#pragma unroll 2
+                    for (int j = 0; j < copies; ++j) {
+                        const int r = 2 * j + half;
+                        const int even = __shfl_sync(0xffffffffu, (j & 1) ? row[t][2] : row[t][0], j >> 1);
+                        const int odd = __shfl_sync(0xffffffffu, (j & 1) ? row[t][3] : row[t][1], j >> 1);
+                        const int from = half ? odd : even;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                                     "l"(p.Q + (int64_t)max(from, 0) * kD + c * 8), "r"(from >= 0 ? 16 : 0)
+                                     : "memory");
                     }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
                 }
                 if (!ok) break;
                 if (ui == 0) publish();
+                // each tile as it lands, from the generic to the tensor cores' view
+                if (tiles == 2) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    fence_proxy_async_smem();
+                    warp_arrive(&sm.q_full[0]);
+                }
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                fence_proxy_async_smem();
+                warp_arrive(&sm.q_full[few ? qb : tiles - 1]);
             }
         }
-        // the last Q loads land before the CTA may exit
-        for (int t = 0; t < kQT; ++t)
-            if ((t ? q_fill[1] : q_fill[0]) > 0) mbar_wait(&sm.q_full[t], ((t ? q_fill[1] : q_fill[0]) - 1) & 1);
     } else if (warp == 3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: O += P V
@@ -1093,7 +1107,7 @@ cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
     const bool gather = page < 8;
     const int64_t q_rows = (int64_t)s.T * s.h, kv_rows = (int64_t)a.num_pages * page * s.g;
     if (q_rows >= ((int64_t)1 << 31) - 1 || (gather && kv_rows >= ((int64_t)1 << 31) - 1)) return cudaErrorNotSupported;
-    CUtensorMap mapK, mapV, mapQ;
+    CUtensorMap mapK, mapV;
     const uint64_t row_bytes = kD * 2;
     const uint32_t row_box[2] = {64, 1};
     if (gather) {
@@ -1107,13 +1121,11 @@ cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
         if (!make_bf16_map(&mapK, a.K_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
         if (!make_bf16_map(&mapV, a.V_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    const uint64_t qdims[2] = {(uint64_t)kD, (uint64_t)q_rows};
-    if (!make_bf16_map(&mapQ, a.Q, 2, qdims, &row_bytes, row_box)) return cudaErrorInvalidValue;
 
     Params p;
+    p.Q = (const bf16*)a.Q;
     p.O = (bf16*)a.O;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)kD);
-    p.q_rows = (int)q_rows;
     p.kv_rows = (int)kv_rows;
     const size_t smem = sizeof(Smem) + 1024;
     auto kern = gather ? chunk_tc_kernel<true> : chunk_tc_kernel<false>;
@@ -1129,7 +1141,7 @@ cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, mapK, mapV, mapQ, u, p);
+    return cudaLaunchKernelEx(&cfg, kern, mapK, mapV, u, p);
 }
 
 }  // namespace gqe
