@@ -5,137 +5,190 @@
 namespace gqe {
 namespace {
 
-// After the tile kernel: block (c, y) of a kind
-//  1. takes again the rows of CTA c's whole units whose result is not finite
-//     (only if the CTA has flagged one): see chunk_row;
+// After the tile kernel, block c, of either kind of units:
+//  1. takes again the rows of CTA c's whole units whose result is not finite (only
+//     if the CTA has flagged one): see chunk_row;
 //  2. merges the split unit whose first steps part c holds as its last:
 //     O = gate * sum_p 2^(lse_p - M) o_p / sum_p 2^(lse_p - M) over its parts in
-//     order (reproducible), one warp per row, rows y apart.
-constexpr int kCombineWarps = 8;
+//     order (reproducible).
+// One block per part: with blocks by part and row range, most of them with nothing
+// to do, 20 us went by on their starting and leaving.
+constexpr int kCombineWarps = 16;
 
-// A unit's row from the formula into O.
+// The rows of a unit whose result is not finite from the formula, a warp each.
 template <typename T, int D>
-__device__ __noinline__ void row_again(const ChunkGeom& u, const ChunkItem& it, int r, int head, const T* Q, const T* Kp,
-                                       const T* Vp, float scale_log2, T* O) {
-    const int lane = threadIdx.x & 31, token = it.t0 + r / u.k;
-    const int64_t row = ((int64_t)token * u.h + head) * D;
-    float acc[D / 32], m, l;
-    chunk_row<T, D>(u, it, it.p0 + r / u.k, Q + row, Kp, Vp, scale_log2, acc, m, l);
-    const float f = u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] / l;
+__device__ __noinline__ void unit_again(const ChunkGeom& u, const ChunkItem& it, int warp, const T* Q, const T* Kp,
+                                        const T* Vp, float scale_log2, T* O) {
+    const int lane = threadIdx.x & 31;
+    for (int r = warp; r < it.nt * u.k; r += kCombineWarps) {
+        const int token = it.t0 + r / u.k;
+        const int64_t at = ((int64_t)token * u.g + it.q) * u.k + r % u.k;
+        const int j = u.idx[at];
+        if (j < it.q * u.hpg || j >= (it.q + 1) * u.hpg) continue;
+        const int64_t row = ((int64_t)token * u.h + j) * D;
+        float check = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) O[row + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
+        for (int e = 0; e < D / 32; ++e) check += 0.f * Elem<T>::to_f(O[row + e * 32 + lane]);
+        if (__all_sync(0xffffffffu, check == 0.f)) continue;
+        float acc[D / 32], m, l;
+        chunk_row<T, D>(u, it, it.p0 + r / u.k, Q + row, Kp, Vp, scale_log2, acc, m, l);
+        const float f = u.gate[at] / l;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) O[row + e * 32 + lane] = Elem<T>::from_f(acc[e] * f);
+    }
 }
 
+// N consecutive elements, N = 4, 2 or 1.
+__device__ __forceinline__ void load_lane(const float* p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void load_lane(const float* p, float (&f)[2]) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    f[0] = v.x, f[1] = v.y;
+}
+__device__ __forceinline__ void load_lane(const float* p, float (&f)[1]) { f[0] = *p; }
+__device__ __forceinline__ void store_lane(float* p, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store_lane(float* p, const float (&f)[2]) {
+    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+}
+__device__ __forceinline__ void store_lane(float* p, const float (&f)[1]) { *p = f[0]; }
+__device__ __forceinline__ void store_lane(__nv_bfloat16* p, const float (&f)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+}
+__device__ __forceinline__ void store_lane(__nv_bfloat16* p, const float (&f)[2]) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
+}
+__device__ __forceinline__ void store_lane(__nv_bfloat16* p, const float (&f)[1]) { *p = __float2bfloat16_rn(f[0]); }
+
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kCombineWarps)
-chunk_combine_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
+__global__ void __launch_bounds__(32 * kCombineWarps, 1)
+chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
                      float scale_log2, T* __restrict__ O) {
+    constexpr int kRec = D + 4, kPer = D / 32, kRows = 4;
+    __shared__ int list[2][kChunkMaxParts];  // by kind: the unit's records in order
+    __shared__ int count[2];
+    __shared__ ChunkDesc desc[2];
+    __shared__ ChunkSplit split;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kRec = D + 4, kPer = D / 32, kRows = 4;
-    __shared__ int list[kChunkMaxParts];  // the unit's records in order
-    __shared__ int count;
-    __shared__ ChunkSplit split;
-    const int c = blockIdx.x, kind = c < u.parts ? 0 : 1, cta = c - kind * u.parts, end = (kind + 1) * u.parts;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const ChunkDesc d = u.desc[2 * c + 1];
-    const bool odd = u.odd[c] != 0;
-    if (warp == 0) {
-        int n = 1;
-        if (lane == 0) list[0] = d.rec;
+    bool odd = false;
+    if (warp < 2) {  // warp `kind` finds the unit and its parts
+        const int c = warp * u.parts + blockIdx.x, end = (warp + 1) * u.parts;
+        const ChunkDesc d = u.desc[2 * c + 1];
+        odd = lane == 0 && u.odd[c] != 0;
+        int n = d.valid ? 1 : 0;
         for (int p0 = c + 1; p0 < end; p0 += 32) {
             const int p = p0 + lane;
             bool mine = false, other = p >= end;
             ChunkDesc e;
             if (p < end) {
                 e = u.desc[2 * p];  // in flight with d
-                mine = e.valid && e.q == d.q && e.t0 == d.t0 && e.b == d.b;
+                mine = d.valid && e.valid && e.q == d.q && e.t0 == d.t0 && e.b == d.b;
                 other = e.valid && !mine;
             }
             const unsigned in = __ballot_sync(0xffffffffu, mine), out = __ballot_sync(0xffffffffu, other);
-            if (mine) list[n + __popc(in & ((1u << lane) - 1u))] = e.rec;
+            if (mine) list[warp][n + __popc(in & ((1u << lane) - 1u))] = e.rec;
             n += __popc(in);
             if (out || !d.valid) break;  // a later unit's part: this unit's are all behind
         }
-        if (lane == 0) count = n;
+        if (lane == 0) {
+            list[warp][0] = d.rec;
+            count[warp] = n;
+            desc[warp] = d;
+        }
     }
-    if (odd) {
-        chunk_split<32 * kCombineWarps>(u, split, cta);
-        ChunkWalk walk(u, split, kind, cta);
+    if (__syncthreads_or(odd)) {
+        for (int kind = 0; kind < 2; ++kind) {
+            if (!u.odd[kind * u.parts + blockIdx.x]) continue;  // the same for the whole block
+            // the flags are by CTA
+            chunk_split<32 * kCombineWarps>(u, split, blockIdx.x);
+            ChunkWalk walk(u, split, kind, blockIdx.x);
+            ChunkItem it;
+            while (walk.next(u, it, false))
+                if (it.rec < 0) unit_again<T, D>(u, it, warp, Q, Kp, Vp, scale_log2, O);
+            __syncthreads();  // split may be overwritten
+        }
+    }
+    bool bad[2] = {false, false};
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const int n = count[kind], rows = n ? desc[kind].nt * u.k : 0;
+        for (int r0 = warp * kRows; r0 < rows; r0 += kCombineWarps * kRows) {
+            const ChunkDesc& d = desc[kind];
+            // kRows rows and two parts at once, all their loads in flight together (with
+            // the maxima in a pass of their own, and a row's loads after another's, 45 us
+            // for 38 MB of records); lane holds elements kPer * lane ..  The running
+            // maximum, sum and row take the parts in order.
+            int to[kRows];  // the row of O, or -1
+            float gate[kRows], M[kRows], L[kRows], acc[kRows][kPer];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = min(r0 + i, rows - 1), token = d.t0 + (r * u.inv_k >> 16);
+                const int64_t at = ((int64_t)token * u.g + d.q) * u.k + r - (r * u.inv_k >> 16) * u.k;
+                to[i] = u.idx[at];
+                gate[i] = u.gate[at];
+                M[i] = -INFINITY;
+                L[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
+            }
+            for (int p = 0; p < n; p += 2) {
+                float lse[2][kRows], v[2][kRows][kPer];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float* rec0 = u.part + (int64_t)list[kind][min(p + x, n - 1)] * kRec;
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+                        const float* rec = rec0 + min(r0 + i, rows - 1) * kRec;
+                        lse[x][i] = p + x < n ? rec[D] : -INFINITY;
+                        load_lane(rec + lane * kPer, v[x][i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    // a log-sum-exp of -inf: no key of the row in that part
+                    const float m = fmaxf(fmaxf(lse[0][i], lse[1][i]), M[i]), ref = m == -INFINITY ? 0.f : m;
+                    const float w = fast_exp2(M[i] - ref), a = fast_exp2(lse[0][i] - ref), b = fast_exp2(lse[1][i] - ref);
+                    M[i] = m;
+                    L[i] = L[i] * w + a + b;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e)
+                        acc[i][e] = acc[i][e] * w + (lse[0][i] == -INFINITY ? 0.f : v[0][i][e] * a) +
+                                    (lse[1][i] == -INFINITY ? 0.f : v[1][i][e] * b);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = r0 + i;
+                const bool in = r < rows && to[i] >= d.q * u.hpg && to[i] < (d.q + 1) * u.hpg;
+                to[i] = in ? (d.t0 + (r * u.inv_k >> 16)) * u.h + to[i] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (to[i] < 0) continue;
+                const float f = gate[i] / L[i];
+                float check = L[i] * 0.f;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    check += acc[i][e] * 0.f;
+                    acc[i][e] *= f;
+                }
+                if (!(check == 0.f)) bad[kind] = true;
+                store_lane(O + (int64_t)to[i] * D + lane * kPer, acc[i]);
+            }
+        }
+    }
+    for (int kind = 0; kind < 2; ++kind) {
+        if (!__syncthreads_or(kind ? bad[1] : bad[0])) continue;
+        const ChunkDesc d = desc[kind];
+        const ChunkSeq s = chunk_seq(u, d.b);
         ChunkItem it;
-        while (walk.next(u, it, false)) {
-            if (it.rec >= 0) continue;
-            for (int r = blockIdx.y * kCombineWarps + warp; r < it.nt * u.k; r += gridDim.y * kCombineWarps) {
-                const int token = it.t0 + r / u.k, j = u.idx[((int64_t)token * u.g + it.q) * u.k + r % u.k];
-                if (j < it.q * u.hpg || j >= (it.q + 1) * u.hpg) continue;
-                float check = 0.f;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) check += 0.f * Elem<T>::to_f(O[((int64_t)token * u.h + j) * D + e * 32 + lane]);
-                if (__any_sync(0xffffffffu, !(check == 0.f))) row_again<T, D>(u, it, r, j, Q, Kp, Vp, scale_log2, O);
-            }
-        }
-    }
-    if (!d.valid) return;
-    __syncthreads();
-    const int n = count, rows = d.nt * u.k;
-    for (int r0 = (blockIdx.y * kCombineWarps + warp) * kRows; r0 < rows; r0 += gridDim.y * kCombineWarps * kRows) {
-        // kRows rows at once, so that their loads are in flight together
-        int j[kRows];
-        float gate[kRows], M[kRows], L[kRows], acc[kRows][kPer];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = min(r0 + i, rows - 1), token = d.t0 + r / u.k;
-            const int64_t at = ((int64_t)token * u.g + d.q) * u.k + r % u.k;
-            j[i] = u.idx[at];
-            gate[i] = u.gate[at];
-            M[i] = -INFINITY;
-            L[i] = 0.f;
-            for (int p = lane; p < n; p += 32) M[i] = fmaxf(M[i], u.part[(int64_t)(list[p] + r) * kRec + D]);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], s));
-#pragma unroll 2
-        for (int p = 0; p < n; ++p) {
-            float lse[kRows], v[kRows][kPer];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const float* rec = u.part + (int64_t)(list[p] + min(r0 + i, rows - 1)) * kRec;
-                lse[i] = rec[D];
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) v[i][e] = rec[e * 32 + lane];
-            }
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (lse[i] == -INFINITY) continue;  // this part holds no key of the row
-                const float w = fast_exp2(lse[i] - M[i]);
-                L[i] += w;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[i][e] = fmaf(v[i][e], w, acc[i][e]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i, token = d.t0 + r / u.k;
-            if (r >= rows || j[i] < d.q * u.hpg || j[i] >= (d.q + 1) * u.hpg) continue;  // no such row
-            float check = L[i] * 0.f;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) check += acc[i][e] * 0.f;
-            if (__any_sync(0xffffffffu, !(check == 0.f))) {
-                const ChunkSeq s = chunk_seq(u, d.b);
-                ChunkItem it;
-                chunk_item(u, s, d.b, d.q, (d.t0 - s.t0) / u.WU, it);
-                row_again<T, D>(u, it, r, j[i], Q, Kp, Vp, scale_log2, O);
-                continue;
-            }
-            const float f = gate[i] / L[i];
-#pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                O[((int64_t)token * u.h + j[i]) * D + e * 32 + lane] = Elem<T>::from_f(acc[i][e] * f);
-        }
+        chunk_item(u, s, d.b, d.q, (d.t0 - s.t0) / u.WU, it);
+        unit_again<T, D>(u, it, warp, Q, Kp, Vp, scale_log2, O);
     }
 }
 
@@ -198,9 +251,10 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     // No more than one unit per token, nor than the full ones and one per request.
     int64_t units = (s.T + u.WU - 1) / u.WU + (int64_t)a.n_seqs;
     if (units > s.T) units = s.T;
-    u.unit_cost = (float)t.unit_keys;
+    u.unit_cost[0] = (float)t.unit_keys;
+    u.unit_cost[1] = (float)t.few_keys;
     u.cost_scale = 1.0f / 16;
-    while ((double)units * s.g * ((double)u.cap + u.WU + t.unit_keys) * u.cost_scale + (double)units * s.g > 2.0e9)
+    while ((double)units * s.g * ((double)u.cap + u.WU + t.unit_keys + t.few_keys) * u.cost_scale + (double)units * s.g > 2.0e9)
         u.cost_scale *= 0.5f;
     u.per_min = 1.0f / (t.min_keys * u.cost_scale);
     u.num_pages = a.num_pages;
@@ -218,9 +272,9 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
 }
 
 template <typename T>
-cudaError_t launch_combine(const ChunkGeom& u, const ChunkArgs& a, int kinds, int blocks) {
+cudaError_t launch_combine(const ChunkGeom& u, const ChunkArgs& a) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kinds * u.parts, blocks);
+    cfg.gridDim = dim3(u.parts);
     cfg.blockDim = dim3(32 * kCombineWarps);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
@@ -253,10 +307,8 @@ cudaError_t launch_chunk(const ChunkArgs& a) {
     const ChunkGeom u = make_geom(a, t, parts);
     const cudaError_t err = on_tensor_cores(a.s) ? launch_chunk_tc(u, a) : launch_chunk_simt(u, a);
     if (err != cudaSuccess) return err;
-    const int blocks = (u.row_cap + 4 * kCombineWarps - 1) / (4 * kCombineWarps);  // about four rows a warp
-    const int kinds = t.few > 0 ? 2 : 1;
-    return a.s->dtype == GQE_BF16 ? launch_combine<__nv_bfloat16>(u, a, kinds, blocks)
-                                  : launch_combine<float>(u, a, kinds, blocks);
+    return a.s->dtype == GQE_BF16 ? launch_combine<__nv_bfloat16>(u, a)
+                                  : launch_combine<float>(u, a);
 }
 
 }  // namespace gqe

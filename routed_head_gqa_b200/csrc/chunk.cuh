@@ -44,7 +44,7 @@ struct ChunkGeom {
     int W, WU;        // tokens per query tile and per unit
     int BN, bn_shift; // keys per step and their log2
     int align;        // rows that the parts of a unit's key list are aligned to
-    float unit_cost;  // a unit's fixed cost, in keys
+    float unit_cost[2];  // a unit's fixed cost, in keys, by kind
     float cost_scale; // requests' costs are summed in whole multiples of 1 / cost_scale keys: 32 bits hold a step's
     float per_min;    // 1 / the smallest cost worth a part
     int few_tokens;   // new tokens up to which a request is of the second kind
@@ -114,9 +114,11 @@ __device__ __forceinline__ int chunk_units(const ChunkGeom& u, int n) { return (
 struct ChunkCost {
     float first, span, grow;  // units before `grow` still grow
     __device__ __forceinline__ ChunkCost(const ChunkGeom& u, const ChunkSeq& s)
-        : first((float)(s.L - s.n + min(s.n, u.WU)) + u.unit_cost), span(0.f), grow(3.4e38f) {
+        : span(0.f), grow(3.4e38f) {
+        const float fixed = chunk_kind(u, s.n) ? u.unit_cost[1] : u.unit_cost[0];
+        first = (float)(s.L - s.n + min(s.n, u.WU)) + fixed;
         if (u.window) {
-            span = (float)u.window + (float)(u.WU + u.sinks) + u.unit_cost;
+            span = (float)u.window + (float)(min(s.n, u.WU) + u.sinks) + fixed;
             grow = ceilf(fmaxf(__fdividef(span - first, (float)u.WU), 0.f));
         }
     }
@@ -438,10 +440,10 @@ size_t chunk_scratch_bytes(const gqe_shape* s);
 cudaError_t launch_chunk(const ChunkArgs& a);
 
 // How a kernel tiles its units: query rows per tile, tiles per unit, the rows up
-// to which a request is of the second kind, keys per step, a unit's fixed cost and
-// the smallest part in keys, blocks per SM.
+// to which a request is of the second kind, keys per step, a unit's fixed cost of
+// either kind and the smallest part in keys, blocks per SM.
 struct ChunkTiling {
-    int rows, tiles, few, keys, unit_keys, min_keys, per_sm;
+    int rows, tiles, few, keys, unit_keys, few_keys, min_keys, per_sm;
 };
 ChunkTiling chunk_simt_tiling();
 cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a);

@@ -264,7 +264,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-chunk_simt_kernel(const ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
+chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
                   T* __restrict__ O, float scale_log2) {
     using C = SimtCfg<T, D>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -316,7 +316,7 @@ cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a) {
 
 }  // namespace
 
-ChunkTiling chunk_simt_tiling() { return {kBM, 1, 0, kBN, 2 * kBN, 4 * kBN, 2}; }
+ChunkTiling chunk_simt_tiling() { return {kBM, 1, 0, kBN, 2 * kBN, 0, 4 * kBN, 2}; }
 
 cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a) {
     const bool bf = a.s->dtype == GQE_BF16;

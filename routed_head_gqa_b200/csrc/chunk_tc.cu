@@ -1087,7 +1087,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
 
 }  // namespace
 
-ChunkTiling chunk_tc_tiling() { return {kBM, kQT, kFew, kBN, 2 * kBN, 4 * kBN, 1}; }
+ChunkTiling chunk_tc_tiling() { return {kBM, kQT, kFew, kBN, 5 * kBN, kBN, 2 * kBN, 1}; }
 
 cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
     const gqe_shape& s = *a.s;
