@@ -214,6 +214,7 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
     const int per = u.n_seqs <= kThreads ? 1 : (u.n_seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, u.n_seqs), b1 = min(b0 + per, u.n_seqs);
     uint32_t mine[2] = {0, 0};
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const ChunkSeq s = chunk_seq(u, b);
         const uint32_t cost = chunk_cost(u, s);
@@ -252,6 +253,7 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
             const uint32_t x = __umulhi(total, (uint32_t)(__fdividef((float)(c + e), (float)parts) * 4294967296.f));
             if (x < before || x - before >= own) continue;
             uint32_t at = before;
+#pragma unroll 1
             for (int b = b0; b < b1; ++b) {
                 const ChunkSeq s = chunk_seq(u, b);
                 const uint32_t cost = chunk_kind(u, s.n) == kind ? chunk_cost(u, s) : 0;

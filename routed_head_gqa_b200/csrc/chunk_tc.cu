@@ -107,14 +107,35 @@ struct Params {
 };
 
 __device__ __forceinline__ bool aborted(Smem& sm) { return *((volatile int32_t*)&sm.abort_flag) != 0; }
-__device__ __forceinline__ void fail(Smem& sm, const ChunkGeom& u, uint32_t detail) {
-    atomicExch(&sm.abort_flag, 1);
-    report_error(u.status, GQE_ERR_DEVICE_TIMEOUT, kWhereChunkTc, detail);
+// Bounded wait of at most kWaitTimeoutNs, in few instructions: the roles wait in
+// some fifty places, and a kernel that outgrows the instruction cache (253 KB with
+// mbar_wait and the error report at each of them) pays for it at every change of
+// phase, 1.7 times the time of the steps around a unit's ends.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u64 t0, t;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t0, %%globaltimer;\n"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u64 t, %%globaltimer;\n\tsub.u64 t, t, t0;\n\tsetp.lt.u64 q, t, %4;\n\t"
+        "@q bra AGAIN;\n"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs), "l"(kWaitTimeoutNs)
+        : "memory");
+    return ok != 0;
 }
-// The whole warp waits; false (reported once) if the wait ran out for any lane.
-__device__ __forceinline__ bool warp_wait(Smem& sm, const ChunkGeom& u, uint64_t* bar, uint32_t parity, uint32_t detail) {
-    if (__all_sync(0xffffffffu, mbar_wait(bar, parity))) return true;
-    if ((threadIdx.x & 31) == 0) fail(sm, u, detail);
+// A wait that ran out: every role stops at its next item, and the kernel reports
+// the place when it ends.
+__device__ __forceinline__ void fail(Smem& sm, int32_t detail) { *((volatile int32_t*)&sm.abort_flag) = detail; }
+// The whole warp waits; false if the wait ran out for any lane.
+__device__ __forceinline__ bool warp_wait(Smem& sm, uint64_t* bar, uint32_t parity, int32_t detail) {
+    if (__all_sync(0xffffffffu, bar_wait(bar, parity))) return true;
+    fail(sm, detail);
     return false;
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -236,12 +257,13 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
     // the four warps of the group have written what the others read next
     auto meet = [&]() {
         warp_arrive(&sm.vote[t]);
-        const bool ok = warp_wait(sm, u, &sm.vote[t], votes & 1, 46);
+        const bool ok = warp_wait(sm, &sm.vote[t], votes & 1, 46);
         ++votes;
         return ok;
     };
+#pragma unroll 1
     for (int i = 0; i < n; ++i, ++ctile) {
-        if (!warp_wait(sm, u, &sm.s_full[t], ctile & 1, 47)) return false;
+        if (!warp_wait(sm, &sm.s_full[t], ctile & 1, 47)) return false;
         tc_fence_after();
         uint32_t s[16];
         tmem_ld16(s_addr, s);
@@ -291,7 +313,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
             }
         }
         // P_t and O^T_t: free once the group's previous product has completed
-        if (ctile > 0 && !warp_wait(sm, u, &sm.p_empty[t], (ctile - 1) & 1, 48)) return false;
+        if (ctile > 0 && !warp_wait(sm, &sm.p_empty[t], (ctile - 1) & 1, 48)) return false;
         if (rescale) {
             tc_fence_after();
             uint32_t o[16];
@@ -320,7 +342,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
     }
     uint32_t o[16];
     if (n > 0) {
-        if (!warp_wait(sm, u, &sm.o_full[t], o_it & 1, 49)) return false;
+        if (!warp_wait(sm, &sm.o_full[t], o_it & 1, 49)) return false;
         ++o_it;
         tc_fence_after();
         tmem_ld16(o_addr, o);
@@ -344,7 +366,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
     }
     if (steps > 1) {  // both groups took part: group 1 hands its state to group 0
         if (t == 1) {
-            if (!warp_wait(sm, u, &sm.x_free, (swaps & 1) ^ 1, 50)) return false;
+            if (!warp_wait(sm, &sm.x_free, (swaps & 1) ^ 1, 50)) return false;
             ++swaps;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -357,7 +379,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
             warp_arrive(&sm.x_full);
             return true;
         }
-        if (!warp_wait(sm, u, &sm.x_full, swaps & 1, 51)) return false;
+        if (!warp_wait(sm, &sm.x_full, swaps & 1, 51)) return false;
         ++swaps;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -449,15 +471,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             tma_prefetch_desc(&mapK);
             tma_prefetch_desc(&mapV);
         }
+#pragma unroll 1
         for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
             const int slot = ui % kItems;
-            if (!warp_wait(sm, u, &sm.item_full[slot], (ui / kItems) & 1, 1)) break;
+            if (!warp_wait(sm, &sm.item_full[slot], (ui / kItems) & 1, 1)) break;
             if (!sm.has[slot]) {
                 warp_arrive(&sm.item_free[slot]);
                 if (++ends == phases) break;
                 continue;
             }
             const ChunkItem it = sm.item[slot];
+#pragma unroll 1
             for (int s = it.s0; s < it.s1; ++s, ++kv_it) {
                 const int st = kv_it & 1, x0 = s * kBN;
                 const uint32_t par = ((kv_it >> 1) & 1) ^ 1;
@@ -485,12 +509,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         tma_load_4d(map, bar, dst + half * kHalf + (lane >> 1) * box_rows * 128, half * 64, it.q, in_page, page);
                     }
                 };
-                if (!warp_wait(sm, u, &sm.kv_empty_k[st], par, 2)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.kv_empty_k[st], par, 2)) { ok = false; break; }
                 if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full_k[st], kTileBytes);
                 __syncwarp();
                 load(&mapK, &sm.kv_full_k[st], sm.k[st]);
                 k_pending = true;
-                if (!warp_wait(sm, u, &sm.kv_empty_v[st], par, 3)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.kv_empty_v[st], par, 3)) { ok = false; break; }
                 if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full_v[st], kTileBytes);
                 __syncwarp();
                 load(&mapV, &sm.kv_full_v[st], sm.v[st]);
@@ -499,11 +523,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             warp_arrive(&sm.item_free[slot]);
         }
         // Drain: every issued load lands before the CTA may exit.
-        if (k_pending) mbar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1);
+        if (k_pending) bar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1);
         for (uint32_t back = 1; back <= 2 && back <= kv_it; ++back) {
             const uint32_t i = kv_it - back;
-            mbar_wait(&sm.kv_full_k[i & 1], (i >> 1) & 1);
-            mbar_wait(&sm.kv_full_v[i & 1], (i >> 1) & 1);
+            bar_wait(&sm.kv_full_k[i & 1], (i >> 1) & 1);
+            bar_wait(&sm.kv_full_v[i & 1], (i >> 1) & 1);
         }
     } else if (warp == 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
@@ -515,13 +539,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             uint32_t kv_it = 0, s_cnt = 0, st_cnt[kQT] = {0, 0};
             bool ok = true;
             // the S buffer is free: its last reader of either form is done
-            auto s_buffer = [&]() { return s_cnt == 0 || mbar_wait(&sm.s_free, (s_cnt - 1) & 1); };
-            auto st_buffer = [&](int t) { return st_cnt[t] == 0 || mbar_wait(&sm.st_free[t], (st_cnt[t] - 1) & 1); };
+            auto s_buffer = [&]() { return s_cnt == 0 || bar_wait(&sm.s_free, (s_cnt - 1) & 1); };
+            auto st_buffer = [&](int t) { return st_cnt[t] == 0 || bar_wait(&sm.st_free[t], (st_cnt[t] - 1) & 1); };
             bool few = few_first;
             uint32_t q_use[kQT] = {0, 0}, few_it = 0;  // fills of the Q buffers so far; few-row items
-            for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
+    #pragma unroll 1
+        for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
                 const int slot = ui % kItems;
-                if (!mbar_wait(&sm.item_full[slot], (ui / kItems) & 1)) { fail(sm, u, 10); break; }
+                if (!bar_wait(&sm.item_full[slot], (ui / kItems) & 1)) { fail(sm, 10); break; }
                 if (!sm.has[slot]) {
                     mbar_arrive(&sm.item_free[slot]);
                     if (++ends == phases) break;
@@ -537,24 +562,26 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const uint32_t q_lo = qb ? q_lo1 : q_lo0;
                 for (int t = 0; t < kQT && ok; ++t) {
                     if (few ? t != qb : t > 0 && tiles < 2) continue;
-                    ok = mbar_wait(&sm.q_full[t], (t ? q_use[1] : q_use[0]) & 1);
+                    ok = bar_wait(&sm.q_full[t], (t ? q_use[1] : q_use[0]) & 1);
                     if (t) ++q_use[1]; else ++q_use[0];
                 }
-                if (!ok) { fail(sm, u, 11); break; }
-                if (few ? !s_buffer() : !(st_buffer(0) && st_buffer(1))) { fail(sm, u, 14); break; }
+                if (!ok) { fail(sm, 11); break; }
+                if (few ? !s_buffer() : !(st_buffer(0) && st_buffer(1))) { fail(sm, 14); break; }
+#pragma unroll 1
                 for (int i = 0; i < n && ok; ++i, ++kv_it) {
-                    if (!mbar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1)) { fail(sm, u, 12); ok = false; break; }
+                    if (!bar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1)) { fail(sm, 12); ok = false; break; }
                     if (few) {
                         const int t = i & 1;
-                        if (!st_buffer(t)) { fail(sm, u, 15); ok = false; break; }
+                        if (!st_buffer(t)) { fail(sm, 15); ok = false; break; }
                         tc_fence_after();
                         issue_st(tmem, dhi, t, q_lo, (kv_it & 1) ? k_lo1 : k_lo0);
                         umma_commit(&sm.s_full[t]);
                         if (t) ++st_cnt[1]; else ++st_cnt[0];
                     }
+#pragma unroll 1
                     for (int t = 0; t < kQT && !few; ++t) {
                         if (i >= (t ? n1 : n0)) continue;
-                        if (!s_buffer()) { fail(sm, u, 13); ok = false; break; }
+                        if (!s_buffer()) { fail(sm, 13); ok = false; break; }
                         tc_fence_after();
                         issue_s(tmem, dhi, t ? q_lo1 : q_lo0, (kv_it & 1) ? k_lo1 : k_lo0);
                         umma_commit(&sm.s_full[t]);
@@ -568,7 +595,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 if (few ? qb == 1 : tiles == 2) umma_commit(&sm.q_empty[1]);
             }
             umma_commit(&sm.mma_drain);  // all issued MMAs complete before TMEM is released
-            mbar_wait(&sm.mma_drain, 0);
+            bar_wait(&sm.mma_drain, 0);
         }
     } else if (warp == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
@@ -589,9 +616,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         for (int phase = 0; phase < phases && ok; ++phase) {
             const bool few = (phase == 0) == few_first;
             ChunkWalk walk(u, sm.split, few, blockIdx.x);
+#pragma unroll 1
             for (; !aborted(sm); ++ui) {
                 const int slot = ui % kItems;
-                if (!warp_wait(sm, u, &sm.item_free[slot], ((ui / kItems) & 1) ^ 1, 20)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.item_free[slot], ((ui / kItems) & 1) ^ 1, 20)) { ok = false; break; }
                 ChunkItem it;
                 const bool has = walk.next(u, it);  // the same in every lane
                 if (!has) {  // every barrier of the ring sees every entry
@@ -638,7 +666,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 for (int t = 0; t < kQT; ++t) {
                     const int buf = few ? qb : t;
                     if (t >= tiles) continue;
-                    if (!warp_wait(sm, u, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
+                    if (!warp_wait(sm, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
                     if (buf) ++q_fill[1]; else ++q_fill[0];
                     // Copy j moves rows 2 j and 2 j + 1, half a warp each, to the 128-byte
                     // swizzled tile; lane r / 4 holds row r.
@@ -680,9 +708,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         uint32_t kv_it = 0, c[kQT] = {0, 0}, o_cnt[kQT] = {0, 0};
         bool ok = true;
         bool few = few_first;
+#pragma unroll 1
         for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
             const int slot = ui % kItems;
-            if (!warp_wait(sm, u, &sm.item_full[slot], (ui / kItems) & 1, 30)) break;
+            if (!warp_wait(sm, &sm.item_full[slot], (ui / kItems) & 1, 30)) break;
             if (!sm.has[slot]) {
                 warp_arrive(&sm.item_free[slot]);
                 if (++ends == phases) break;
@@ -692,8 +721,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const ChunkItem it = sm.item[slot];
             warp_arrive(&sm.item_free[slot]);
             const int n = it.s1 - it.s0, n0 = tile_steps(u, it, 0, few), n1 = tile_steps(u, it, 1, few);
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i, ++kv_it) {
-                if (!warp_wait(sm, u, &sm.kv_full_v[kv_it & 1], (kv_it >> 1) & 1, 31)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.kv_full_v[kv_it & 1], (kv_it >> 1) & 1, 31)) { ok = false; break; }
                 // Rows of loaded pages that no row of the unit sees: past the last
                 // token, and between the first `sinks` keys and the window.
                 const int x0 = (it.s0 + i) * kBN, x1 = x0 + kBN;  // of the key list
@@ -702,6 +732,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     auto zero = [&](int a, int b) {
                         a = max(a, x0);
                         b = min(b, x1);
+#pragma unroll 1
                         for (int x = lane; x < (b - a) * 16; x += 32)
                             *reinterpret_cast<uint4*>(v + ((x & 8) ? kHalf : 0) + (a - x0 + (x >> 4)) * 128 + (x & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
@@ -714,11 +745,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
+#pragma unroll 1
                 for (int t = 0; t < kQT; ++t) {
                     const int j = few ? i >> 1 : i;  // the group's own step
                     if (few ? (i & 1) != t : i >= (t ? n1 : n0)) continue;
-                    if (!warp_wait(sm, u, &sm.p_full[t], c[t] & 1, 32)) { ok = false; break; }
-                    if (j == 0 && !warp_wait(sm, u, &sm.o_empty[t], (o_cnt[t] & 1) ^ 1, 33)) { ok = false; break; }
+                    if (!warp_wait(sm, &sm.p_full[t], c[t] & 1, 32)) { ok = false; break; }
+                    if (j == 0 && !warp_wait(sm, &sm.o_empty[t], (o_cnt[t] & 1) ^ 1, 33)) { ok = false; break; }
                     if (lane == 0) {
                         tc_fence_after();
                         const uint32_t v_lo = (kv_it & 1) ? v_lo1 : v_lo0;
@@ -739,7 +771,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         }
         if (lane == 0) {
             umma_commit(&sm.mma_drain2);
-            mbar_wait(&sm.mma_drain2, 0);
+            bar_wait(&sm.mma_drain2, 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -759,7 +791,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         uint32_t ui = 0;
         // The next item of the kind, or null at its end (or after a failure).
         auto take = [&]() -> const ChunkItem* {
-            if (aborted(sm) || !warp_wait(sm, u, &sm.item_full[ui % kItems], (ui / kItems) & 1, 40)) return nullptr;
+            if (aborted(sm) || !warp_wait(sm, &sm.item_full[ui % kItems], (ui / kItems) & 1, 40)) return nullptr;
             if (sm.has[ui % kItems]) return &sm.item[ui % kItems];
             warp_arrive(&sm.item_free[ui++ % kItems]);
             return nullptr;
@@ -773,12 +805,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const int32_t* heads = sm.row_j[ui % kItems][t] + (r - sel);
             bf16* o = p.O + ((int64_t)(it.t0 + off) * u.h + it.q * u.hpg) * kD;
             int turn = 0;
+#pragma unroll 1
             for (int a0 = 0; a0 < u.hpg; a0 += 32) {
                 uint32_t free = low_bits(u.hpg - a0);
+#pragma unroll 1
                 for (int a = 0; a < u.k; ++a) {
                     const int j = heads[a] - it.q * u.hpg - a0;
                     if (j >= 0 && j < 32) free &= ~(1u << j);
                 }
+#pragma unroll 1
                 for (; free; free &= free - 1) {
                     if (turn == sel)
                         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
@@ -796,7 +831,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             while (const ChunkItem* next = take()) {
                 const ChunkItem it = *next;
                 const int slot = ui % kItems;
-                if (!warp_wait(sm, u, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
+                if (!warp_wait(sm, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
                 if (t == 0) zero_fill(it, it.nt);
                 if (!(it.nt * u.k <= 4 ? few_item<4>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)
                                        : few_item<16>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)))
@@ -804,7 +839,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 done();
             }
             // group 0 has read what group 1 handed over: x is the stages' now
-            if (swaps > 0 && !aborted(sm)) warp_wait(sm, u, &sm.x_free, (swaps - 1) & 1, 52);
+            if (swaps > 0 && !aborted(sm)) warp_wait(sm, &sm.x_free, (swaps - 1) & 1, 52);
             continue;
         }
         while (const ChunkItem* next = take()) {
@@ -814,7 +849,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const int toks = min(it.nt - t * u.W, u.W);  // of this tile; 0 or less: none
             // Every item's rows_full phase is waited for in turn, as a later one may
             // complete before a waiter of the same parity looks.
-            if (!warp_wait(sm, u, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
+            if (!warp_wait(sm, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
             if (toks <= 0) {
                 done();
                 continue;
@@ -834,11 +869,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             const int x_first = it.s0 * kBN, skip = it.skip;
+#pragma unroll 1
             for (int i = 0; i < n; ++i, ++ctile) {
-                if (!warp_wait(sm, u, &sm.s_full[t], ctile & 1, 42)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.s_full[t], ctile & 1, 42)) { ok = false; break; }
                 if (!live) {  // no query row: hand both buffers on, P no sooner than the slot is free
                     if (lane == 0) mbar_arrive(&sm.s_free);
-                    if (ctile > 0 && !warp_wait(sm, u, &sm.p_empty[t], (ctile - 1) & 1, 45)) { ok = false; break; }
+                    if (ctile > 0 && !warp_wait(sm, &sm.p_empty[t], (ctile - 1) & 1, 45)) { ok = false; break; }
                     if (lane == 0) mbar_arrive(&sm.p_full[t]);
                     continue;
                 }
@@ -860,7 +896,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 // P slot of this tile: free once the tile's previous P.V has
                 // completed (which also completes O_t up to the previous step).
                 auto wait_slot = [&]() {
-                    if (ctile > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.p_empty[t], (ctile - 1) & 1))) slot_ok = false;
+                    if (ctile > 0 && !__all_sync(0xffffffffu, bar_wait(&sm.p_empty[t], (ctile - 1) & 1))) slot_ok = false;
                     tc_fence_after();
                 };
                 // Hide what a row does not see: per 32 keys a bit each, applied where some
@@ -977,7 +1013,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 tc_fence_before();
                 warp_arrive(&sm.p_full[t]);
                 if (!slot_ok) {
-                    if (lane == 0) fail(sm, u, 43);
+                    if (lane == 0) fail(sm, 43);
                     ok = false;
                     break;
                 }
@@ -993,7 +1029,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 done();
                 continue;
             }
-            if (!warp_wait(sm, u, &sm.o_full[t], o_it & 1, 44)) break;
+            if (!warp_wait(sm, &sm.o_full[t], o_it & 1, 44)) break;
             ++o_it;
             if (!live) {
                 warp_arrive(&sm.o_empty[t]);
@@ -1022,20 +1058,28 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 if (partial) u.part[(int64_t)(rec_row + lane) * (kD + 4) + kD] = none ? -INFINITY : m + log2f(l);
             }
             uint4* stage = sm.stage(t, wq);
-            // Writes 64 bytes of every row of the warp: to[row] + byte offset
-            auto flush = [&](const uint4 (&v)[4], auto address) {
+            // This lane's 16 bytes of four of the warp's rows: 8 e + lane / 4.
+            uint4* to[4];
+            const int out_row = head >= 0 ? token * u.h + head : -1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 8 * e + (lane >> 2), there = __shfl_sync(0xffffffffu, out_row, row);
+                to[e] = there < 0 ? nullptr
+                        : partial ? reinterpret_cast<uint4*>(u.part + (int64_t)(rec_row + row) * (kD + 4)) + (lane & 3)
+                                  : reinterpret_cast<uint4*>(p.O + (int64_t)there * kD) + (lane & 3);
+            }
+            // Writes 64 bytes (piece cb) of every row of the warp.
+            auto flush = [&](const uint4 (&v)[4], int cb) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) stage[lane * 4 + (c ^ ((lane >> 1) & 3))] = v[c];
                 __syncwarp();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int row = 8 * e + (lane >> 2), c = lane & 3;
-                    uint4* to = address(row, c);
-                    if (to) *to = stage[row * 4 + (c ^ ((row >> 1) & 3))];
+                    const int row = 8 * e + (lane >> 2);
+                    if (to[e]) to[e][cb * 4] = stage[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
                 }
                 __syncwarp();
             };
-            const int out_row = head >= 0 ? token * u.h + head : -1;
             if (partial) {
 #pragma unroll
                 for (int cb = 0; cb < 8; ++cb) {
@@ -1046,11 +1090,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         v[c] = make_uint4(__float_as_uint(__uint_as_float(w[0]) * f), __float_as_uint(__uint_as_float(w[1]) * f),
                                           __float_as_uint(__uint_as_float(w[2]) * f), __float_as_uint(__uint_as_float(w[3]) * f));
                     }
-                    flush(v, [&](int row, int c) -> uint4* {
-                        const int there = __shfl_sync(0xffffffffu, out_row, row);
-                        return there < 0 ? nullptr
-                                         : reinterpret_cast<uint4*>(u.part + (int64_t)(rec_row + row) * (kD + 4) + cb * 16) + c;
-                    });
+                    flush(v, cb);
                 }
             } else {
 #pragma unroll
@@ -1064,10 +1104,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         v[c].z = pack_bf16x2(__uint_as_float(w[4]) * f, __uint_as_float(w[5]) * f);
                         v[c].w = pack_bf16x2(__uint_as_float(w[6]) * f, __uint_as_float(w[7]) * f);
                     }
-                    flush(v, [&](int row, int c) -> uint4* {
-                        const int there = __shfl_sync(0xffffffffu, out_row, row);
-                        return there < 0 ? nullptr : reinterpret_cast<uint4*>(p.O + (int64_t)there * kD + cb * 32) + c;
-                    });
+                    flush(v, cb);
                 }
             }
             done();
@@ -1083,6 +1120,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    if (tid == 0 && sm.abort_flag != 0)
+        report_error(u.status, GQE_ERR_DEVICE_TIMEOUT, kWhereChunkTc, (uint32_t)sm.abort_flag);
 }
 
 }  // namespace
