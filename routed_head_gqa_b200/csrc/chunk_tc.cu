@@ -882,9 +882,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 uint32_t s[4][32];
                 const int x0 = x_first + i * kBN, kv0 = x0 + skip;  // of the key list; its key behind the first ones
                 const bool need_mask = kv0 + kBN - 1 > pos_first || kv0 < low_last;
-                uint64_t sum2[4] = {0, 0, 0, 0};
-                float m_use = m;
-                bool done = false, slot_ok = true;
+                uint64_t sum2[4];
 #pragma unroll
                 for (int cb = 0; cb < 4; ++cb) tmem_ld32(s_addr + cb * 32, s[cb]);
                 ld_wait_bind(s[0]);
@@ -893,12 +891,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 ld_bind(s[3]);
                 tc_fence_before();
                 warp_arrive(&sm.s_free);
-                // P slot of this tile: free once the tile's previous P.V has
-                // completed (which also completes O_t up to the previous step).
-                auto wait_slot = [&]() {
-                    if (ctile > 0 && !__all_sync(0xffffffffu, bar_wait(&sm.p_empty[t], (ctile - 1) & 1))) slot_ok = false;
-                    tc_fence_after();
-                };
                 // Hide what a row does not see: per 32 keys a bit each, applied where some
                 // of the warp's rows need it.
                 if (need_mask) {
@@ -917,13 +909,32 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         }
                     }
                 }
-                // After the first step the exponentials are taken against the running
-                // max while the step's row max is formed alongside: unless some row of
-                // the warp grew its max by more than the threshold, P is final.
-                if (i > 0) {
-                    const uint64_t NM2 = pk2(-m, -m);
+                // The exponentials are taken against the running max while the step's row
+                // max is formed alongside: unless some row of the warp grew its max by
+                // more than the threshold, P is final; else O_t and the row's sum are
+                // rescaled and the exponentials taken once more.  An item's first step
+                // forms the max beforehand.
+                if (i == 0) {
                     float mq[4];
-                    uint32_t pk[4][16];
+#pragma unroll
+                    for (int cb = 0; cb < 4; ++cb) {
+                        float a0 = __uint_as_float(s[cb][0]);
+#pragma unroll
+                        for (int e = 1; e < 31; e += 2)
+                            a0 = fmax3(a0, __uint_as_float(s[cb][e]), __uint_as_float(s[cb][e + 1]));
+                        mq[cb] = fmaxf(a0, __uint_as_float(s[cb][31]));
+                    }
+                    m = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * p.scale_log2;
+                }
+                bool slot_ok = true, slot_free = false;
+#pragma unroll 1
+                while (true) {
+                    const float ref = m == -INFINITY ? 0.f : m;  // no key seen so far: weights of 0
+                    const uint64_t NM2 = pk2(-ref, -ref);
+                    float mq[4];
+                    uint32_t pk[2][16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum2[e] = 0;
 #pragma unroll
                     for (int cb = 0; cb < 4; ++cb) {
                         float a0 = __uint_as_float(s[cb][0]);
@@ -937,46 +948,31 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                             up2(ffma2(pk2(__uint_as_float(s[cb][2 * e]), __uint_as_float(s[cb][2 * e + 1])), C2, NM2), x0, x1);
                             const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
                             sum2[e & 3] = fadd2(sum2[e & 3], pk2(p0, p1));
-                            pk[cb][e] = pack_bf16x2(p0, p1);
+                            pk[cb & 1][e] = pack_bf16x2(p0, p1);
                         }
-                        // the first two chunks wait in registers for the slot
+                        // The first two chunks wait in registers for the tile's P slot: free
+                        // once its previous P.V has completed (and with it O_t so far).
                         if (cb == 1) {
-                            wait_slot();
+                            if (!slot_free) {
+                                slot_free = true;
+                                if (ctile > 0 && !__all_sync(0xffffffffu, bar_wait(&sm.p_empty[t], (ctile - 1) & 1))) slot_ok = false;
+                                tc_fence_after();
+                            }
                             tmem_st16(p_addr, pk[0]);
                             tmem_st16(p_addr + 16, pk[1]);
                         } else if (cb > 1) {
-                            tmem_st16(p_addr + cb * 16, pk[cb]);
+                            tmem_st16(p_addr + cb * 16, pk[cb & 1]);
                         }
                     }
                     const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * p.scale_log2;
-                    done = __all_sync(0xffffffffu, mx <= m + kRescaleThreshold);
-                    if (!done) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum2[e] = 0;
-                    }
-                }
-                if (!done) {
-                    float mq[4];
-#pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        float a0 = __uint_as_float(s[cb][0]);
-#pragma unroll
-                        for (int e = 1; e < 31; e += 2)
-                            a0 = fmax3(a0, __uint_as_float(s[cb][e]), __uint_as_float(s[cb][e + 1]));
-                        mq[cb] = fmaxf(a0, __uint_as_float(s[cb][31]));
-                    }
-                    const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * p.scale_log2;
-                    // Lazy rescaling: keep the running max unless it grows by more
-                    // than the threshold.  A row that has seen no key so far has
-                    // weights 0 only, and O_t rows of 0: nothing to rescale.
-                    bool rescale = false;
-                    if (mx > m + kRescaleThreshold || m == -INFINITY) {
-                        m_use = mx;
-                        rescale = m != -INFINITY;
-                    }
-                    wait_slot();
-                    if (__any_sync(0xffffffffu, rescale)) {
-                        const float alpha = rescale ? fast_exp2(m - m_use) : 1.0f;
+                    // A row whose max was still -inf has weights taken against 0: right only
+                    // if it still sees nothing.
+                    const bool grown = m == -INFINITY ? mx != -INFINITY : mx > m + kRescaleThreshold;
+                    if (__all_sync(0xffffffffu, !grown)) break;
+                    const float alpha = grown && m != -INFINITY ? fast_exp2(m - mx) : 1.0f;  // -inf: O_t's row is 0
+                    if (grown) m = mx;
+                    l *= alpha;
+                    if (i > 0) {
 #pragma unroll 1
                         for (int cb = 0; cb < 4; ++cb) {
                             uint32_t o[32];
@@ -987,28 +983,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                             tmem_st16(o_addr + cb * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
                             tmem_st16(o_addr + cb * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
                         }
-                        l *= alpha;
-                    }
-                    const float ref = m_use == -INFINITY ? 0.f : m_use;
-                    const uint64_t NM2 = pk2(-ref, -ref);
-#pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float x0, x1;
-                            up2(ffma2(pk2(__uint_as_float(s[cb][2 * e]), __uint_as_float(s[cb][2 * e + 1])), C2, NM2), x0, x1);
-                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                            sum2[e & 3] = fadd2(sum2[e & 3], pk2(p0, p1));
-                            pk[e] = pack_bf16x2(p0, p1);
-                        }
-                        tmem_st16(p_addr + cb * 16, pk);
                     }
                 }
                 float sa, sb;
                 up2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])), sa, sb);
                 l += sa + sb;
-                m = m_use;
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(&sm.p_full[t]);
