@@ -82,23 +82,16 @@ struct ChunkSeq {
 // A request's rows, or none (n = 0) when its entries contradict each other
 // (reported): rows outside the packed tensor, a cache shorter than the new
 // tokens or longer than the block table.
-__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkGeom& u, int b) {
-    ChunkSeq s;
-    s.t0 = u.cu[b];
-    const int t1 = u.cu[b + 1];
-    s.L = u.lengths[b];
-    s.n = 0;
-    if (s.t0 < 0 || t1 < s.t0 || t1 > u.T) {
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkGeom& u, int b, int t0, int t1, int L) {
+    ChunkSeq s = {t0, t1 - t0, L};
+    if (t0 < 0 || t1 < t0 || t1 > u.T || (s.n > 0 && (L < s.n || L > u.cap))) {
         report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)b);
-        return s;
+        s.n = 0;
     }
-    const int n = t1 - s.t0;
-    if (n > 0 && (s.L < n || s.L > u.cap)) {
-        report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)b);
-        return s;
-    }
-    s.n = n;
     return s;
+}
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkGeom& u, int b) {
+    return chunk_seq(u, b, u.cu[b], u.cu[b + 1], u.lengths[b]);
 }
 
 // 0: many query rows, 1: few.
@@ -195,6 +188,7 @@ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkGeom& u, const Chun
 struct ChunkEnd {
     int b;
     float fraction;
+    ChunkSeq seq;
 };
 struct ChunkSplit {
     uint32_t warp_sum[2][32];
@@ -220,7 +214,7 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
         const uint32_t cost = chunk_cost(u, s);
         if (chunk_kind(u, s.n)) mine[1] += cost; else mine[0] += cost;
     }
-    if (tid < 4) sp.end[tid >> 1][tid & 1] = {u.n_seqs, 0.f};  // overwritten below where the place exists
+    if (tid < 4) sp.end[tid >> 1][tid & 1].b = u.n_seqs;  // overwritten below where the place exists
     uint32_t run[2] = {mine[0], mine[1]};
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -258,7 +252,7 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
                 const ChunkSeq s = chunk_seq(u, b);
                 const uint32_t cost = chunk_kind(u, s.n) == kind ? chunk_cost(u, s) : 0;
                 if (x - at < cost) {
-                    sp.end[kind][e] = {b, __fdividef((float)(x - at), (float)cost)};
+                    sp.end[kind][e] = {b, __fdividef((float)(x - at), (float)cost), s};
                     break;
                 }
                 at += cost;
@@ -268,60 +262,78 @@ __device__ __forceinline__ void chunk_split(const ChunkGeom& u, ChunkSplit& sp, 
     __syncthreads();
 }
 
-// Walks a CTA's items of a kind in order.  Warp-collective: the lanes hold 32
-// requests, so that a run of short ones costs one round of loads.
+// Walks a CTA's items of a kind in order.  Warp-collective: the lanes hold the
+// entries of 32 requests, so that a run of short ones costs one round of loads,
+// which the first item (whose request the split has left) does not wait for.
 struct ChunkWalk {
     ChunkPlace at, to;
-    ChunkSeq held;       // request base + lane
+    ChunkSeq seq;        // of request at.b
+    int t0, t1, L;       // entries of request base + lane
     int kind, base, part;
     __device__ __forceinline__ ChunkWalk(const ChunkGeom& u, const ChunkSplit& sp, int kind, int cta)
-        : kind(kind), base(-64), part(chunk_part(u, kind, cta)) {
+        : kind(kind), part(chunk_part(u, kind, cta)) {
+        base = sp.end[kind][0].b;
+        fetch(u);
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 1; i >= 0; --i) {
+            to = at;
             const ChunkEnd e = sp.end[kind][i];
-            at = to;
-            to = {u.n_seqs, 0, 0, 0};
-            if (e.b < u.n_seqs) to = chunk_place(u, chunk_seq(u, e.b), e.b, e.fraction);
+            at = {u.n_seqs, 0, 0, 0};
+            if (e.b < u.n_seqs) at = chunk_place(u, e.seq, e.b, e.fraction);
+            seq = e.seq;
+        }
+    }
+    __device__ __forceinline__ void fetch(const ChunkGeom& u) {
+        const int b = base + (threadIdx.x & 31);
+        t0 = t1 = L = 0;
+        if (b < u.n_seqs) {
+            t0 = u.cu[b];
+            t1 = u.cu[b + 1];
+            L = u.lengths[b];
         }
     }
     // describe: write the descriptors of split units
     __device__ __forceinline__ bool next(const ChunkGeom& u, ChunkItem& it, bool describe = true) {
-        const int lane = threadIdx.x & 31;
-        while (true) {
-            if (at.b >= u.n_seqs || at.b > to.b) return false;
-            if (at.b < base || at.b >= base + 32) {
-                base = at.b;
-                held = {0, 0, 0};
-                if (base + lane < u.n_seqs) held = chunk_seq(u, base + lane);
-                if (chunk_kind(u, held.n) != kind) held.n = 0;
+        if (at.b >= u.n_seqs) return false;
+        if (at.i >= chunk_units(u, seq.n)) {
+            at.i = 0;
+            if (++at.q >= u.g) {  // the next request that has work of this kind
+                at.q = 0;
+                int src = at.b - base + 1;
+                while (true) {
+                    if (src >= 32) {
+                        base += 32;
+                        if (base >= u.n_seqs || base > to.b) return false;
+                        fetch(u);
+                        src = 0;
+                    }
+                    const ChunkSeq s = chunk_seq(u, base + (threadIdx.x & 31), t0, t1, L);
+                    const unsigned some = __ballot_sync(0xffffffffu, s.n > 0 && chunk_kind(u, s.n) == kind) >> src;
+                    if (some) {
+                        src += __ffs(some) - 1;
+                        seq = {__shfl_sync(0xffffffffu, s.t0, src), __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.L, src)};
+                        break;
+                    }
+                    src = 32;
+                }
+                at.b = base + src;
             }
-            const int src = at.b - base;
-            const ChunkSeq seq = {__shfl_sync(0xffffffffu, held.t0, src), __shfl_sync(0xffffffffu, held.n, src),
-                                  __shfl_sync(0xffffffffu, held.L, src)};
-            const int units = chunk_units(u, seq.n);
-            if (at.i >= units && ++at.q < u.g && units > 0) {
-                at.i = 0;
-            } else if (at.i >= units) {  // the next request that has work of this kind, if it is among the held
-                const unsigned some = __ballot_sync(0xffffffffu, held.n > 0) & ~(src == 31 ? 0xffffffffu : (2u << src) - 1u);
-                at = {some ? base + __ffs(some) - 1 : base + 32, 0, 0, 0};
-                continue;
-            }
-            const bool last = at.b == to.b && at.q == to.q && at.i == to.i;
-            if (at.b == to.b && (at.q > to.q || (at.q == to.q && at.i > to.i))) return false;
-            if (last && at.s >= to.s) return false;
-            chunk_item(u, seq, at.b, at.q, at.i, it);
-            it.s0 = at.s;
-            it.s1 = last ? min(to.s, it.steps) : it.steps;
-            it.rec = -1;
-            if (it.s0 > 0 || it.s1 < it.steps) {
-                const int slot = it.s0 > 0 ? 2 * part : 2 * part + 1;
-                it.rec = kind ? 2 * u.parts * u.row_cap + slot * u.few_cap : slot * u.row_cap;
-                if (lane == 0 && describe) u.desc[kind * 2 * u.parts + slot] = {1, it.b, it.q, it.t0, it.nt, it.rec};
-            }
-            ++at.i;
-            at.s = 0;
-            return true;
         }
+        if (at.b > to.b || (at.b == to.b && (at.q > to.q || (at.q == to.q && at.i > to.i)))) return false;
+        const bool last = at.b == to.b && at.q == to.q && at.i == to.i;
+        if (last && at.s >= to.s) return false;
+        chunk_item(u, seq, at.b, at.q, at.i, it);
+        it.s0 = at.s;
+        it.s1 = last ? min(to.s, it.steps) : it.steps;
+        it.rec = -1;
+        if (it.s0 > 0 || it.s1 < it.steps) {
+            const int slot = it.s0 > 0 ? 2 * part : 2 * part + 1;
+            it.rec = kind ? 2 * u.parts * u.row_cap + slot * u.few_cap : slot * u.row_cap;
+            if ((threadIdx.x & 31) == 0 && describe) u.desc[kind * 2 * u.parts + slot] = {1, it.b, it.q, it.t0, it.nt, it.rec};
+        }
+        ++at.i;
+        at.s = 0;
+        return true;
     }
 };
 

@@ -648,9 +648,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     }
                     __syncwarp();
                 };
-                // The first item's K/V loads queue up behind its Q rows, not before
-                // them; later ones need not wait for the Q buffers to be free.
-                if (ui > 0) publish();
+                // Many rows: the first item's K/V loads queue up behind its Q rows, not
+                // before them; else they need not wait for the Q buffers to be free.
+                const bool early = few || ui > 0;
+                if (early) publish();
 #pragma unroll
                 for (int t = 0; t < kQT; ++t)
 #pragma unroll
@@ -686,7 +687,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     asm volatile("cp.async.commit_group;" ::: "memory");
                 }
                 if (!ok) break;
-                if (ui == 0) publish();
+                if (!early) publish();
                 // each tile as it lands, from the generic to the tensor cores' view
                 if (tiles == 2) {
                     asm volatile("cp.async.wait_group 1;" ::: "memory");
