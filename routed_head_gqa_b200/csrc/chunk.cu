@@ -201,7 +201,7 @@ int device_sms() {
 
 size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
 
-bool on_tensor_cores(const gqe_shape* s) { return s->dtype == GQE_BF16 && s->d_h == 128; }
+bool on_tensor_cores(const gqe_shape* s) { return s->dtype == GQE_BF16; }
 
 ChunkTiling tiling(const gqe_shape* s) { return on_tensor_cores(s) ? chunk_tc_tiling() : chunk_simt_tiling(); }
 

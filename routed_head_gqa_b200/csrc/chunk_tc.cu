@@ -1,5 +1,5 @@
 // chunk_tc.cu -- routed attention of ragged chunks of new tokens over a paged
-// cache on the sm_100a tensor cores (bf16, d_h = 128), with an optional sliding
+// cache on the sm_100a tensor cores (bf16, d_h = 128, 64 or 32), with an optional sliding
 // window.  See chunk.cuh for the units, the schedule and the masks.
 //
 // A unit has up to two query tiles of 128 rows (W = floor(128 / k) tokens of k
@@ -13,8 +13,8 @@
 //
 // Roles (384 threads, one persistent CTA per SM):
 //   warp 0      K/V tiles by TMA: one box per page (of at most 128 rows) and
-//               64-column half, lane by lane; pages of fewer than 8 rows by
-//               tile::gather4.  Pages that no row of the unit sees are loaded
+//               64-column half, lane by lane; pages of fewer than 16 rows by 16-byte
+//               asynchronous copies.  Pages that no row of the unit sees are loaded
 //               from outside the pool, which the TMA fills with zeros.
 //   warp 1      MMA issuer (one thread): S_t = Q_t K^T
 //   warp 2      walks the part's items (a ring of 4), gathers the routed rows of Q
@@ -50,11 +50,10 @@ namespace {
 using namespace sm100;
 using bf16 = __nv_bfloat16;
 
-constexpr int kD = 128, kBM = 128, kBN = 128, kQT = 2, kThreads = 384;
+constexpr int kBM = 128, kBN = 128, kQT = 2, kThreads = 384;
 constexpr int kFew = 16;                   // query rows up to which a unit is turned around
 constexpr int kItems = 4;                  // items in flight between the walk and the other roles
-constexpr uint32_t kHalf = 128 * 64 * 2;   // one [128][64] bf16 box, 16 KB
-constexpr uint32_t kTileBytes = 2 * kHalf;
+constexpr uint32_t kHalf = 128 * 64 * 2;   // 64 elements of 128 rows, 16 KB
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: p <= 2^8 between rescales
@@ -63,19 +62,24 @@ constexpr uint32_t kWhereChunkTc = 11;     // status "where" id of this kernel
 constexpr int kRegsLaunch = 168, kRegsCtl = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsCtl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split exceeds the launch");
 
+// kH: a head in 64-element parts, two (d_h = 128) or one (d_h = 64, or 32 in one
+// padded with zeros).
+template <int kH>
 struct Smem {
-    uint8_t q[kQT][kTileBytes];
-    uint8_t k[2][kTileBytes];
-    uint8_t v[2][kTileBytes];
+    static constexpr uint32_t kTile = kH * kHalf;  // bytes of a Q, K or V tile
+    static constexpr int kStages = 4 / kH;         // K and V tiles in flight, each
+    uint8_t q[kQT][kTile];
+    uint8_t k[kStages][kTile];
+    uint8_t v[kStages][kTile];
     uint8_t p[kQT][kFew * 256];          // few rows: P_t [16 rows][128 keys] bf16, two 64-key halves
-    float x[kFew][kD];                   // few rows: O^T_1 on its way to warpgroup 0
+    float x[kFew][128];                  // few rows: O^T_1 on its way to warpgroup 0
     // Many rows: 64 bytes of each of a softmax warp's 32 rows on their way out, in a
     // half of the group's own p and of x.
     __device__ __forceinline__ uint4* stage(int t, int w) {
         return reinterpret_cast<uint4*>(w < 2 ? p[t] + w * 2048 : reinterpret_cast<uint8_t*>(x) + t * 4096 + (w - 2) * 2048);
     }
     float x_ml[2][kFew];                 //   with its maxima and sums
-    uint4 zero[kD * 2 / 16];             // a row of zeros, for the unselected output slots
+    uint4 zero[16];                     // a row of zeros, for the unselected output slots
     float4 wmax[kQT][2][kFew];           // few rows: the four warps' maxima of a step
     float4 wsum[kQT][kFew];              //   and their sums at the end
     ChunkItem item[kItems];
@@ -84,7 +88,7 @@ struct Smem {
     ChunkSplit split;
     // barriers, in the order of kBarCounts
     uint64_t item_full[kItems], rows_full[kItems], item_free[kItems];
-    uint64_t kv_full_k[2], kv_full_v[2], kv_empty_k[2], kv_empty_v[2];
+    uint64_t kv_full_k[kStages], kv_full_v[kStages], kv_empty_k[kStages], kv_empty_v[kStages];
     uint64_t s_full[kQT], p_empty[kQT], o_full[kQT], q_full[kQT], q_empty[kQT], p_full[kQT], o_empty[kQT], st_free[kQT], vote[kQT];
     uint64_t x_full, x_free, s_free, mma_drain, mma_drain2;
     uint32_t tmem_base;
@@ -92,21 +96,28 @@ struct Smem {
 };
 
 // Arrivals that complete a barrier: 11 readers of an item (warps 0, 1, 3 and the
-// eight softmax warps), the four warps of a warpgroup, or one.
+// eight softmax warps), 32 lanes of gathered K/V rows, the four warps of a
+// warpgroup, or one.
+template <int kH, bool kGather>
 __device__ __forceinline__ uint32_t bar_count(int i) {
-    constexpr int kFree = 2 * kItems, kOnes = 3 * kItems, kWarps = kOnes + 8 + 5 * kQT, kTail = kWarps + 4 * kQT + 3;
-    return i < kFree ? 1 : i < kOnes ? 11 : i < kWarps ? 1 : i < kTail ? 4 : 1;
+    constexpr int kS = Smem<kH>::kStages, kFree = 2 * kItems, kLoads = 3 * kItems, kOnes = kLoads + 2 * kS,
+                  kWarps = kOnes + 2 * kS + 5 * kQT, kTail = kWarps + 4 * kQT + 3;
+    return i < kFree ? 1 : i < kLoads ? 11 : i < kOnes ? (kGather ? 32 : 1) : i < kWarps ? 1 : i < kTail ? 4 : 1;
 }
-constexpr int kBars = 3 * kItems + 8 + 9 * kQT + 5;
+template <int kH>
+constexpr int bar_total() { return 3 * kItems + 4 * Smem<kH>::kStages + 9 * kQT + 5; }
 
 struct Params {
     const bf16* Q;
     bf16* O;
     float scale_log2;
-    int kv_rows;  // rows of K seen as [num_pages * page_size * g, 128] (gathered pages only)
+    const bf16* K;  // gathered pages only
+    const bf16* V;
+    int d;          // d_h
 };
 
-__device__ __forceinline__ bool aborted(Smem& sm) { return *((volatile int32_t*)&sm.abort_flag) != 0; }
+template <class S>
+__device__ __forceinline__ bool aborted(S& sm) { return *((volatile int32_t*)&sm.abort_flag) != 0; }
 // Bounded wait of at most kWaitTimeoutNs, in few instructions: the roles wait in
 // some fifty places, and a kernel that outgrows the instruction cache (253 KB with
 // mbar_wait and the error report at each of them) pays for it at every change of
@@ -131,9 +142,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
 }
 // A wait that ran out: every role stops at its next item, and the kernel reports
 // the place when it ends.
-__device__ __forceinline__ void fail(Smem& sm, int32_t detail) { *((volatile int32_t*)&sm.abort_flag) = detail; }
+template <class S>
+__device__ __forceinline__ void fail(S& sm, int32_t detail) { *((volatile int32_t*)&sm.abort_flag) = detail; }
 // The whole warp waits; false if the wait ran out for any lane.
-__device__ __forceinline__ bool warp_wait(Smem& sm, uint64_t* bar, uint32_t parity, int32_t detail) {
+template <class S>
+__device__ __forceinline__ bool warp_wait(S& sm, uint64_t* bar, uint32_t parity, int32_t detail) {
     if (__all_sync(0xffffffffu, bar_wait(bar, parity))) return true;
     fail(sm, detail);
     return false;
@@ -183,18 +196,20 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 // S_t = Q_t K(it)^T: eight K steps of 16 over 128-byte swizzled tiles; a step
-// moves the descriptors' start address only.
+// moves the descriptors' start address only (d_h = 64: four).
+template <int kH>
 __device__ __forceinline__ void issue_s(uint32_t tmem, uint32_t dhi, uint32_t q_lo, uint32_t k_lo) {
     constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, false, false);
 #pragma unroll
-    for (int kk = 0; kk < kD / 16; ++kk) {
+    for (int kk = 0; kk < 4 * kH; ++kk) {
         const uint32_t off = (uint32_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
         umma_ss(tmem + kColS, smem_desc_join(q_lo + off, dhi), smem_desc_join(k_lo + off, dhi), idesc, kk > 0 ? 1u : 0u);
     }
 }
 // O_t += P_t V(it), P_t from TMEM, V as an MN-major operand.
+template <int kH>
 __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t dhi, int t, uint32_t v_lo, bool first) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kBM, kD, false, true);
+    constexpr uint32_t idesc = idesc_bf16_f32(kBM, 64 * kH, false, true);
 #pragma unroll
     for (int kk = 0; kk < kBN / 16; ++kk)
         umma_ts(tmem + kColO + t * 128, tmem + kColP + 64 * t + kk * 8, smem_desc_join(v_lo + (uint32_t)((kk * 2048) >> 4), dhi),
@@ -202,17 +217,19 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t dhi, int t, uin
 }
 
 // Few rows: S^T_t = K(it) Q^T, and O^T_t += V(it)^T P_t with V as an MN-major
-// operand of M = 128 elements of the head and P_t from shared memory.
+// operand of M = 128 elements of the head (d_h = 64: the part twice, its leading
+// byte offset 0) and P_t from shared memory.
+template <int kH>
 __device__ __forceinline__ void issue_st(uint32_t tmem, uint32_t dhi, int t, uint32_t q_lo, uint32_t k_lo) {
     constexpr uint32_t idesc = idesc_bf16_f32(kBN, kFew, false, false);
 #pragma unroll
-    for (int kk = 0; kk < kD / 16; ++kk) {
+    for (int kk = 0; kk < 4 * kH; ++kk) {
         const uint32_t off = (uint32_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
         umma_ss(tmem + kColS + 64 * t, smem_desc_join(k_lo + off, dhi), smem_desc_join(q_lo + off, dhi), idesc, kk > 0 ? 1u : 0u);
     }
 }
 __device__ __forceinline__ void issue_pvt(uint32_t tmem, uint32_t dhi, int t, uint32_t v_lo, uint32_t p_lo, bool first) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kD, kFew, true, false);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kFew, true, false);
 #pragma unroll
     for (int kk = 0; kk < kBN / 16; ++kk)
         umma_ss(tmem + kColO + t * 128, smem_desc_join(v_lo + (uint32_t)((kk * 2048) >> 4), dhi),
@@ -234,13 +251,14 @@ __device__ __forceinline__ float warp_sum(float x) {
 // Softmax, epilogue and merge of an item of at most NR rows (few rows), for the
 // warpgroup of tile t.  Each thread holds one key of a step, then one element of
 // the head.  Returns false when a wait ran out.
-template <int NR>
-__device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Smem& sm, const ChunkItem& it, int slot, int t,
+template <int NR, int kH>
+__device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Smem<kH>& sm, const ChunkItem& it, int slot, int t,
                                          uint32_t tmem, uint32_t& ctile, uint32_t& o_it, uint32_t& votes, uint32_t& swaps) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, col = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + kColS + 64 * t, o_addr = tmem + lane_off + kColO + 128 * t;
     const int rows = it.nt * u.k, steps = it.s1 - it.s0, n = tile_steps(u, it, t, true);
+    const int d = kH == 2 ? 128 : p.d;
     const bool partial = it.rec >= 0;
     // gate of row `lane`, in flight until the epilogue
     float gate = 0.f;
@@ -398,38 +416,72 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
     for (int r = 0; r < NR; ++r) {
         const int head = r < rows ? sm.row_j[slot][0][r] : -1;
         const float gm = __shfl_sync(0xffffffffu, gate, r);
-        if (head < 0) continue;
+        if (head < 0 || col >= d) continue;
         const float v = __uint_as_float(o[r]);
         check += v * 0.f + l[r] * 0.f;
         if (partial) {
             const bool none = m[r] == -INFINITY && l[r] == 0.f;
-            float* rec = u.part + (int64_t)(it.rec + r) * (kD + 4);
+            float* rec = u.part + (int64_t)(it.rec + r) * (d + 4);
             rec[col] = none ? 0.f : v / l[r];
-            if (col == 0) rec[kD] = none ? -INFINITY : m[r] + log2f(l[r]);
+            if (col == 0) rec[d] = none ? -INFINITY : m[r] + log2f(l[r]);
         } else {
-            p.O[((int64_t)(it.t0 + (r * u.inv_k >> 16)) * u.h + head) * kD + col] = __float2bfloat16_rn(v * (gm / l[r]));
+            p.O[((int64_t)(it.t0 + (r * u.inv_k >> 16)) * u.h + head) * d + col] = __float2bfloat16_rn(v * (gm / l[r]));
         }
     }
     if (!(check == 0.f) && !partial) u.odd[u.parts + blockIdx.x] = 1;
     return true;
 }
 
-// kGather: pages of fewer than 8 rows, fetched row by row.
-template <bool kGather>
+// Copies rows of 64 kH elements (of which d exist, the others zeros) to a 128-byte
+// swizzled tile, 16 bytes a lane, whole rows of adjacent lanes; lane r / 4 holds the
+// index of row r in row[r % 4], -1 for a row of zeros.
+template <int kH>
+__device__ __forceinline__ void copy_rows(uint32_t tile, const bf16* base, int64_t stride, const int (&row)[4], int rows, int d) {
+    constexpr int kPer = 4 / kH;  // rows a copy
+    const int lane = threadIdx.x & 31, sub = lane / (8 * kH), c = lane % (8 * kH);
+    const uint32_t dst = tile + (c >> 3) * kHalf;
+    const bool in = kH == 2 || c * 8 < d;
+#pragma unroll 2
+    for (int j = 0; j < rows / kPer; ++j) {
+        const int r = kPer * j + sub;
+        int from;
+        if constexpr (kH == 2) {
+            const int even = __shfl_sync(0xffffffffu, (j & 1) ? row[2] : row[0], j >> 1);
+            const int odd = __shfl_sync(0xffffffffu, (j & 1) ? row[3] : row[1], j >> 1);
+            from = sub ? odd : even;
+        } else {
+            const int a = __shfl_sync(0xffffffffu, row[0], j), b = __shfl_sync(0xffffffffu, row[1], j);
+            const int e = __shfl_sync(0xffffffffu, row[2], j), f = __shfl_sync(0xffffffffu, row[3], j);
+            from = sub == 0 ? a : sub == 1 ? b : sub == 2 ? e : f;
+        }
+        const bool on = from >= 0 && in;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                     "l"(base + (on ? from * stride + c * 8 : 0)), "r"(on ? 16 : 0)
+                     : "memory");
+    }
+}
+
+// kGather: pages of fewer than 16 rows, fetched row by row.
+template <int kH, bool kGather>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                 const __grid_constant__ ChunkGeom u, const Params p) {
     extern __shared__ uint8_t smem_raw[];
-    Smem& sm = *smem_align1024<Smem>(smem_raw);
+    using S = Smem<kH>;
+    S& sm = *smem_align1024<S>(smem_raw);
+    constexpr int kBars = bar_total<kH>();
+    constexpr uint32_t kTileBytes = S::kTile;
+    constexpr int kStages = S::kStages;
+    const int d = kH == 2 ? 128 : p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     static_assert(kBars <= 64, "one barrier per thread of warps 1 and 2");
     if (warp == 1 || warp == 2) {
-        if (tid - 32 < kBars) mbar_init(&sm.item_full[0] + (tid - 32), bar_count(tid - 32));
+        if (tid - 32 < kBars) mbar_init(&sm.item_full[0] + (tid - 32), bar_count<kH, kGather>(tid - 32));
         fence_barrier_init();
     }
     if (tid == 96) sm.abort_flag = 0;
-    if (warp == 4 && lane < kD * 2 / 16) {
+    if (warp == 4 && lane < 16) {
         sm.zero[lane] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
@@ -463,11 +515,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         // ------------------------------------------------------------ K/V tiles
         const int shift = u.page_shift;
         const int box_rows = shift >= 7 ? kBN : 1 << shift;
-        const int boxes = kBN / box_rows;  // per tile and half
+        const int boxes = kBN / box_rows;  // per tile and 64-element part
         uint32_t kv_it = 0;
         bool k_pending = false;
         bool ok = true;
-        if (lane == 0) {
+        if (!kGather && lane == 0) {
             tma_prefetch_desc(&mapK);
             tma_prefetch_desc(&mapV);
         }
@@ -483,51 +535,52 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const ChunkItem it = sm.item[slot];
 #pragma unroll 1
             for (int s = it.s0; s < it.s1; ++s, ++kv_it) {
-                const int st = kv_it & 1, x0 = s * kBN;
-                const uint32_t par = ((kv_it >> 1) & 1) ^ 1;
+                const int st = kv_it % kStages, x0 = s * kBN;
+                const uint32_t par = ((kv_it / kStages) & 1) ^ 1;
                 int page = 0, in_page = 0, row[4];
                 if constexpr (kGather) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int key = it.key(x0 + lane * 4 + e);
                         const bool on = key < it.hi && (key >= it.lo || key < u.sinks);
-                        row[e] = on ? (int)(chunk_cache_row(u, it.b, key) * u.g + it.q) : p.kv_rows;
+                        row[e] = on ? (int)chunk_cache_row(u, it.b, key) : -1;
                     }
-                } else if (lane < 2 * boxes) {
-                    const int key = it.key(x0 + (lane >> 1) * box_rows);
+                } else if (lane < kH * boxes) {
+                    const int key = it.key(x0 + (lane / kH) * box_rows);
                     const bool on = key < it.hi && (key + box_rows > it.lo || key < u.sinks);
                     page = u.num_pages;  // outside the pool: zeros
                     in_page = key & ((1 << shift) - 1);
                     if (on) page = (int)(chunk_cache_row(u, it.b, key) >> shift);
                 }
-                auto load = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* dst) {
+                auto load = [&](const CUtensorMap* map, const bf16* pages, uint64_t* bar, uint8_t* dst) {
                     if constexpr (kGather) {
-                        tma_gather4_2d(map, bar, dst + lane * 512, 0, row[0], row[1], row[2], row[3]);
-                        tma_gather4_2d(map, bar, dst + kHalf + lane * 512, 64, row[0], row[1], row[2], row[3]);
-                    } else if (lane < 2 * boxes) {
-                        const int half = lane & 1;
-                        tma_load_4d(map, bar, dst + half * kHalf + (lane >> 1) * box_rows * 128, half * 64, it.q, in_page, page);
+                        copy_rows<kH>(smem_u32(dst), pages + (int64_t)it.q * d, (int64_t)u.g * d, row, kBN, d);
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+                    } else {
+                        if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+                        __syncwarp();
+                        if (lane < kH * boxes) {
+                            const int half = lane % kH;
+                            tma_load_4d(map, bar, dst + half * kHalf + (lane / kH) * box_rows * 128, half * 64, it.q, in_page, page);
+                        }
                     }
                 };
                 if (!warp_wait(sm, &sm.kv_empty_k[st], par, 2)) { ok = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full_k[st], kTileBytes);
-                __syncwarp();
-                load(&mapK, &sm.kv_full_k[st], sm.k[st]);
+                load(&mapK, p.K, &sm.kv_full_k[st], sm.k[st]);
                 k_pending = true;
                 if (!warp_wait(sm, &sm.kv_empty_v[st], par, 3)) { ok = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full_v[st], kTileBytes);
-                __syncwarp();
-                load(&mapV, &sm.kv_full_v[st], sm.v[st]);
+                load(&mapV, p.V, &sm.kv_full_v[st], sm.v[st]);
                 k_pending = false;
             }
             warp_arrive(&sm.item_free[slot]);
         }
         // Drain: every issued load lands before the CTA may exit.
-        if (k_pending) bar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1);
-        for (uint32_t back = 1; back <= 2 && back <= kv_it; ++back) {
+        if (k_pending) bar_wait(&sm.kv_full_k[kv_it % kStages], (kv_it / kStages) & 1);
+#pragma unroll 1
+        for (uint32_t back = 1; back <= kStages && back <= kv_it; ++back) {
             const uint32_t i = kv_it - back;
-            bar_wait(&sm.kv_full_k[i & 1], (i >> 1) & 1);
-            bar_wait(&sm.kv_full_v[i & 1], (i >> 1) & 1);
+            bar_wait(&sm.kv_full_k[i % kStages], (i / kStages) & 1);
+            bar_wait(&sm.kv_full_v[i % kStages], (i / kStages) & 1);
         }
     } else if (warp == 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
@@ -535,7 +588,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         if (lane == 0) {
             const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
             const uint32_t q_lo0 = smem_desc_lo(smem_u32(sm.q[0]), 16), q_lo1 = smem_desc_lo(smem_u32(sm.q[1]), 16);
-            const uint32_t k_lo0 = smem_desc_lo(smem_u32(sm.k[0]), 16), k_lo1 = smem_desc_lo(smem_u32(sm.k[1]), 16);
+            const uint32_t k_lo0 = smem_desc_lo(smem_u32(sm.k[0]), 16);
             uint32_t kv_it = 0, s_cnt = 0, st_cnt[kQT] = {0, 0};
             bool ok = true;
             // the S buffer is free: its last reader of either form is done
@@ -569,12 +622,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 if (few ? !s_buffer() : !(st_buffer(0) && st_buffer(1))) { fail(sm, 14); break; }
 #pragma unroll 1
                 for (int i = 0; i < n && ok; ++i, ++kv_it) {
-                    if (!bar_wait(&sm.kv_full_k[kv_it & 1], (kv_it >> 1) & 1)) { fail(sm, 12); ok = false; break; }
+                    const int st = kv_it % kStages;
+                    const uint32_t k_lo = k_lo0 + st * (kTileBytes >> 4);
+                    if (!bar_wait(&sm.kv_full_k[st], (kv_it / kStages) & 1)) { fail(sm, 12); ok = false; break; }
+                    if (kGather) fence_proxy_async_smem();  // rows written by plain copies
                     if (few) {
                         const int t = i & 1;
                         if (!st_buffer(t)) { fail(sm, 15); ok = false; break; }
                         tc_fence_after();
-                        issue_st(tmem, dhi, t, q_lo, (kv_it & 1) ? k_lo1 : k_lo0);
+                        issue_st<kH>(tmem, dhi, t, q_lo, k_lo);
                         umma_commit(&sm.s_full[t]);
                         if (t) ++st_cnt[1]; else ++st_cnt[0];
                     }
@@ -583,12 +639,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         if (i >= (t ? n1 : n0)) continue;
                         if (!s_buffer()) { fail(sm, 13); ok = false; break; }
                         tc_fence_after();
-                        issue_s(tmem, dhi, t ? q_lo1 : q_lo0, (kv_it & 1) ? k_lo1 : k_lo0);
+                        issue_s<kH>(tmem, dhi, t ? q_lo1 : q_lo0, k_lo);
                         umma_commit(&sm.s_full[t]);
                         ++s_cnt;
                     }
                     if (!ok) break;
-                    umma_commit(&sm.kv_empty_k[kv_it & 1]);
+                    umma_commit(&sm.kv_empty_k[st]);
                 }
                 if (!ok) break;
                 if (qb == 0) umma_commit(&sm.q_empty[0]);
@@ -669,21 +725,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (t >= tiles) continue;
                     if (!warp_wait(sm, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
                     if (buf) ++q_fill[1]; else ++q_fill[0];
-                    // Copy j moves rows 2 j and 2 j + 1, half a warp each, to the 128-byte
-                    // swizzled tile; lane r / 4 holds row r.
-                    const int half = lane >> 4, c = lane & 15, copies = few ? kFew / 2 : kBM / 2;
-                    const uint32_t dst = smem_u32(sm.q[buf]) + (c >> 3) * kHalf;
-#pragma unroll 2
-                    for (int j = 0; j < copies; ++j) {
-                        const int r = 2 * j + half;
-                        const int even = __shfl_sync(0xffffffffu, (j & 1) ? row[t][2] : row[t][0], j >> 1);
-                        const int odd = __shfl_sync(0xffffffffu, (j & 1) ? row[t][3] : row[t][1], j >> 1);
-                        const int from = half ? odd : even;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                         dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                                     "l"(p.Q + (int64_t)max(from, 0) * kD + c * 8), "r"(from >= 0 ? 16 : 0)
-                                     : "memory");
-                    }
+                    copy_rows<kH>(smem_u32(sm.q[buf]), p.Q, d, row[t], few ? kFew : kBM, d);
                     asm volatile("cp.async.commit_group;" ::: "memory");
                 }
                 if (!ok) break;
@@ -703,7 +745,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: O += P V
         const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
-        const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v[0]), kHalf), v_lo1 = smem_desc_lo(smem_u32(sm.v[1]), kHalf);
+        const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v[0]), kH == 2 ? kHalf : 0);
         const uint32_t p_lo0 = smem_desc_lo(smem_u32(sm.p[0]), 16), p_lo1 = smem_desc_lo(smem_u32(sm.p[1]), 16);
         const int page = 1 << u.page_shift;
         uint32_t kv_it = 0, c[kQT] = {0, 0}, o_cnt[kQT] = {0, 0};
@@ -724,19 +766,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             const int n = it.s1 - it.s0, n0 = tile_steps(u, it, 0, few), n1 = tile_steps(u, it, 1, few);
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i, ++kv_it) {
-                if (!warp_wait(sm, &sm.kv_full_v[kv_it & 1], (kv_it >> 1) & 1, 31)) { ok = false; break; }
+                const int st = kv_it % kStages;
+                if (!warp_wait(sm, &sm.kv_full_v[st], (kv_it / kStages) & 1, 31)) { ok = false; break; }
+                if (kGather) fence_proxy_async_smem();
                 // Rows of loaded pages that no row of the unit sees: past the last
                 // token, and between the first `sinks` keys and the window.
                 const int x0 = (it.s0 + i) * kBN, x1 = x0 + kBN;  // of the key list
                 if (x1 > it.hi - it.skip || (u.window && x0 < it.lo - it.skip)) {
-                    uint8_t* v = sm.v[kv_it & 1];
+                    uint8_t* v = sm.v[st];
                     auto zero = [&](int a, int b) {
                         a = max(a, x0);
                         b = min(b, x1);
 #pragma unroll 1
-                        for (int x = lane; x < (b - a) * 16; x += 32)
-                            *reinterpret_cast<uint4*>(v + ((x & 8) ? kHalf : 0) + (a - x0 + (x >> 4)) * 128 + (x & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                        for (int x = lane; x < (b - a) * 8 * kH; x += 32)
+                            *reinterpret_cast<uint4*>(v + (kH == 2 && (x & 8) ? kHalf : 0) + (a - x0 + x / (8 * kH)) * 128 +
+                                                      (x & 7) * 16) = make_uint4(0, 0, 0, 0);
                     };
                     zero(it.hi - it.skip, ((it.hi + page - 1) & ~(page - 1)) - it.skip);
                     if (u.window) {
@@ -754,11 +798,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (j == 0 && !warp_wait(sm, &sm.o_empty[t], (o_cnt[t] & 1) ^ 1, 33)) { ok = false; break; }
                     if (lane == 0) {
                         tc_fence_after();
-                        const uint32_t v_lo = (kv_it & 1) ? v_lo1 : v_lo0;
+                        const uint32_t v_lo = v_lo0 + st * (kTileBytes >> 4);
                         if (few)
                             issue_pvt(tmem, dhi, t, v_lo, t ? p_lo1 : p_lo0, j == 0);
                         else
-                            issue_pv(tmem, dhi, t, v_lo, j == 0);
+                            issue_pv<kH>(tmem, dhi, t, v_lo, j == 0);
                         umma_commit(&sm.p_empty[t]);
                         if (j == (t ? n1 : n0) - 1) umma_commit(&sm.o_full[t]);
                     }
@@ -766,7 +810,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (j == 0) ++o_cnt[t];
                 }
                 if (!ok) break;
-                if (lane == 0) umma_commit(&sm.kv_empty_v[kv_it & 1]);
+                if (lane == 0) umma_commit(&sm.kv_empty_v[st]);
                 __syncwarp();
             }
         }
@@ -804,7 +848,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         auto zero_fill = [&](const ChunkItem& it, int toks) {
             if (it.s0 != 0 || u.k == u.hpg || r >= toks * u.k) return;
             const int32_t* heads = sm.row_j[ui % kItems][t] + (r - sel);
-            bf16* o = p.O + ((int64_t)(it.t0 + off) * u.h + it.q * u.hpg) * kD;
+            bf16* o = p.O + ((int64_t)(it.t0 + off) * u.h + it.q * u.hpg) * d;
             int turn = 0;
 #pragma unroll 1
             for (int a0 = 0; a0 < u.hpg; a0 += 32) {
@@ -818,8 +862,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 for (; free; free &= free - 1) {
                     if (turn == sel)
                         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                                         o + (int64_t)(a0 + __ffs(free) - 1) * kD),
-                                     "r"(smem_u32(sm.zero)), "r"(kD * 2)
+                                         o + (int64_t)(a0 + __ffs(free) - 1) * d),
+                                     "r"(smem_u32(sm.zero)), "r"(d * 2)
                                      : "memory");
                     if (++turn == u.k) turn = 0;
                 }
@@ -834,8 +878,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const int slot = ui % kItems;
                 if (!warp_wait(sm, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
                 if (t == 0) zero_fill(it, it.nt);
-                if (!(it.nt * u.k <= 4 ? few_item<4>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)
-                                       : few_item<16>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)))
+                if (!(it.nt * u.k <= 4 ? few_item<4, kH>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)
+                                       : few_item<16, kH>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)))
                     break;
                 done();
             }
@@ -975,7 +1019,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     l *= alpha;
                     if (i > 0) {
 #pragma unroll 1
-                        for (int cb = 0; cb < 4; ++cb) {
+                        for (int cb = 0; cb < 2 * kH; ++cb) {
                             uint32_t o[32];
                             tmem_ld32(o_addr + cb * 32, o);
                             ld_wait_bind(o);
@@ -1005,7 +1049,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             // each row at a time go through shared memory and out as whole sectors.
             const int rec_row = it.rec + t * u.W * u.k + wq * 32;
             if (n == 0) {
-                if (partial && mine) u.part[(int64_t)(rec_row + lane) * (kD + 4) + kD] = -INFINITY;
+                if (partial && mine) u.part[(int64_t)(rec_row + lane) * (d + 4) + d] = -INFINITY;
                 done();
                 continue;
             }
@@ -1017,25 +1061,24 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 continue;
             }
             tc_fence_after();
-            uint32_t o[4][32];
+            uint32_t o[2 * kH][32];
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb) tmem_ld32(o_addr + cb * 32, o[cb]);
+            for (int cb = 0; cb < 2 * kH; ++cb) tmem_ld32(o_addr + cb * 32, o[cb]);
             ld_wait_bind(o[0]);
-            ld_bind(o[1]);
-            ld_bind(o[2]);
-            ld_bind(o[3]);
+#pragma unroll
+            for (int cb = 1; cb < 2 * kH; ++cb) ld_bind(o[cb]);
             tc_fence_before();
             warp_arrive(&sm.o_empty[t]);
             const bool none = m == -INFINITY && l == 0.f;
             const float f = partial ? (none ? 0.f : 1.f / l) : gate / l;
             float check[4] = {l * 0.f, 0.f, 0.f, 0.f};  // stays 0, or NaN when a value is not finite
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb)
+            for (int cb = 0; cb < 2 * kH; ++cb)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) check[e & 3] = fmaf(__uint_as_float(o[cb][e]), 0.f, check[e & 3]);
             if (head >= 0) {
                 if (!partial && !((check[0] + check[1]) + (check[2] + check[3]) == 0.f)) u.odd[blockIdx.x] = 1;
-                if (partial) u.part[(int64_t)(rec_row + lane) * (kD + 4) + kD] = none ? -INFINITY : m + log2f(l);
+                if (partial) u.part[(int64_t)(rec_row + lane) * (d + 4) + d] = none ? -INFINITY : m + log2f(l);
             }
             uint4* stage = sm.stage(t, wq);
             // This lane's 16 bytes of four of the warp's rows: 8 e + lane / 4.
@@ -1045,8 +1088,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             for (int e = 0; e < 4; ++e) {
                 const int row = 8 * e + (lane >> 2), there = __shfl_sync(0xffffffffu, out_row, row);
                 to[e] = there < 0 ? nullptr
-                        : partial ? reinterpret_cast<uint4*>(u.part + (int64_t)(rec_row + row) * (kD + 4)) + (lane & 3)
-                                  : reinterpret_cast<uint4*>(p.O + (int64_t)there * kD) + (lane & 3);
+                        : partial ? reinterpret_cast<uint4*>(u.part + (int64_t)(rec_row + row) * (d + 4)) + (lane & 3)
+                                  : reinterpret_cast<uint4*>(p.O + (int64_t)there * d) + (lane & 3);
             }
             // Writes 64 bytes (piece cb) of every row of the warp.
             auto flush = [&](const uint4 (&v)[4], int cb) {
@@ -1062,7 +1105,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             };
             if (partial) {
 #pragma unroll
-                for (int cb = 0; cb < 8; ++cb) {
+                for (int cb = 0; cb < 4 * kH; ++cb) {
+                    if (kH == 1 && cb * 16 >= d) break;
                     uint4 v[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -1074,7 +1118,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 }
             } else {
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb) {
+                for (int cb = 0; cb < 2 * kH; ++cb) {
+                    if (kH == 1 && cb * 32 >= d) break;
                     uint4 v[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -1108,46 +1153,31 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
 
 ChunkTiling chunk_tc_tiling() { return {kBM, kQT, kFew, kBN, 5 * kBN, kBN, 2 * kBN, 1}; }
 
-cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
-    const gqe_shape& s = *a.s;
-    // The setmaxnreg split needs exactly kRegsLaunch registers per thread at
-    // launch (a property of the compiled kernels: checked once per process).
-    static std::atomic<int> regs_checked{0};
-    if (regs_checked.load(std::memory_order_acquire) == 0) {
-        cudaFuncAttributes fa, fb;
-        cudaError_t e = cudaFuncGetAttributes(&fa, chunk_tc_kernel<false>);
-        if (e == cudaSuccess) e = cudaFuncGetAttributes(&fb, chunk_tc_kernel<true>);
-        if (e != cudaSuccess) return e;
-        regs_checked.store(fa.numRegs == kRegsLaunch && fb.numRegs == kRegsLaunch ? 1 : -1, std::memory_order_release);
-    }
-    if (regs_checked.load(std::memory_order_acquire) != 1) return cudaErrorNotSupported;
+namespace {
 
-    const int page = 1 << a.page_shift;
-    const bool gather = page < 8;
-    const int64_t q_rows = (int64_t)s.T * s.h, kv_rows = (int64_t)a.num_pages * page * s.g;
-    if (q_rows >= ((int64_t)1 << 31) - 1 || (gather && kv_rows >= ((int64_t)1 << 31) - 1)) return cudaErrorNotSupported;
-    CUtensorMap mapK, mapV;
-    const uint64_t row_bytes = kD * 2;
-    const uint32_t row_box[2] = {64, 1};
-    if (gather) {
-        const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)kv_rows};
-        if (!make_bf16_map(&mapK, a.K_pages, 2, dims, &row_bytes, row_box)) return cudaErrorInvalidValue;
-        if (!make_bf16_map(&mapV, a.V_pages, 2, dims, &row_bytes, row_box)) return cudaErrorInvalidValue;
-    } else {
-        const uint64_t dims[4] = {(uint64_t)kD, (uint64_t)s.g, (uint64_t)page, (uint64_t)a.num_pages};
-        const uint64_t strides[3] = {row_bytes, s.g * row_bytes, (uint64_t)page * s.g * row_bytes};
-        const uint32_t box[4] = {64, 1, (uint32_t)(page < kBN ? page : kBN), 1};
-        if (!make_bf16_map(&mapK, a.K_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
-        if (!make_bf16_map(&mapV, a.V_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
-    }
+// The setmaxnreg split draws on the registers of the launch: a property of the
+// compiled kernels, checked once per process.
+template <int kH, bool kGather>
+bool registers_suffice() {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, chunk_tc_kernel<kH, kGather>) == cudaSuccess && f.numRegs >= kRegsLaunch;
+}
 
+template <int kH, bool kGather>
+cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a, const CUtensorMap& mapK, const CUtensorMap& mapV) {
+    static std::atomic<int> state{0};
+    if (state.load(std::memory_order_acquire) == 0)
+        state.store(registers_suffice<kH, kGather>() ? 1 : -1, std::memory_order_release);
+    if (state.load(std::memory_order_acquire) != 1) return cudaErrorNotSupported;
     Params p;
     p.Q = (const bf16*)a.Q;
     p.O = (bf16*)a.O;
-    p.scale_log2 = 1.4426950408889634f / sqrtf((float)kD);
-    p.kv_rows = (int)kv_rows;
-    const size_t smem = sizeof(Smem) + 1024;
-    auto kern = gather ? chunk_tc_kernel<true> : chunk_tc_kernel<false>;
+    p.scale_log2 = 1.4426950408889634f / sqrtf((float)a.s->d_h);
+    p.K = (const bf16*)a.K_pages;
+    p.V = (const bf16*)a.V_pages;
+    p.d = a.s->d_h;
+    const size_t smem = sizeof(Smem<kH>) + 1024;
+    auto kern = chunk_tc_kernel<kH, kGather>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -1161,6 +1191,30 @@ cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, mapK, mapV, u, p);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
+    const gqe_shape& s = *a.s;
+    const int page = 1 << a.page_shift;
+    if ((int64_t)s.T * s.h >= ((int64_t)1 << 31) - 1) return cudaErrorNotSupported;
+    // Pages of 16 rows or more by the TMA, a box per page and 64-element part; of
+    // fewer rows by copies, row by row: at 8 rows a page the boxes' number held 64
+    // decodes at 3.8 TB/s (16 rows: 5.8), at 4 rows the TMA's gather of four rows at a
+    // time at 1.9.
+    const bool gather = page < 16;
+    CUtensorMap mapK{}, mapV{};
+    if (!gather) {
+        const uint64_t row_bytes = (uint64_t)s.d_h * 2;
+        const uint64_t dims[4] = {(uint64_t)s.d_h, (uint64_t)s.g, (uint64_t)page, (uint64_t)a.num_pages};
+        const uint64_t strides[3] = {row_bytes, s.g * row_bytes, (uint64_t)page * s.g * row_bytes};
+        const uint32_t box[4] = {64, 1, (uint32_t)(page < kBN ? page : kBN), 1};
+        if (!make_bf16_map(&mapK, a.K_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!make_bf16_map(&mapV, a.V_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    if (s.d_h == 128) return gather ? launch_typed<2, true>(u, a, mapK, mapV) : launch_typed<2, false>(u, a, mapK, mapV);
+    return gather ? launch_typed<1, true>(u, a, mapK, mapV) : launch_typed<1, false>(u, a, mapK, mapV);
 }
 
 }  // namespace gqe
