@@ -50,7 +50,7 @@ namespace {
 using namespace sm100;
 using bf16 = __nv_bfloat16;
 
-constexpr int kBM = 128, kBN = 128, kQT = 2, kThreads = 384;
+constexpr int kBM = 128, kBN = 128, kQT = 2;
 constexpr int kFew = 16;                   // query rows up to which a unit is turned around
 constexpr int kItems = 4;                  // items in flight between the walk and the other roles
 constexpr uint32_t kHalf = 128 * 64 * 2;   // 64 elements of 128 rows, 16 KB
@@ -58,9 +58,15 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: p <= 2^8 between rescales
 constexpr uint32_t kWhereChunkTc = 11;     // status "where" id of this kernel
-// Register split (setmaxnreg): 4 control warps at 72, 8 softmax warps at 216.
-constexpr int kRegsLaunch = 168, kRegsCtl = 72, kRegsSoftmax = 216;
-static_assert(128 * kRegsCtl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split exceeds the launch");
+// Threads and register split (setmaxnreg): 4 control warps and, for gathered
+// pages, 4 that copy rows; 8 softmax warps.
+template <bool kGather>
+struct Split {
+    static constexpr int kThreads = kGather ? 512 : 384;
+    static constexpr int kRegsLaunch = kGather ? 128 : 168;
+    static constexpr int kRegsCtl = kGather ? 56 : 72, kRegsSoftmax = kGather ? 200 : 216;
+    static_assert((kThreads - 256) * kRegsCtl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "more registers than the launch has");
+};
 
 // kH: a head in 64-element parts, two (d_h = 128) or one (d_h = 64, or 32 in one
 // padded with zeros).
@@ -85,6 +91,7 @@ struct Smem {
     ChunkItem item[kItems];
     int32_t has[kItems];                 // 0: no more items of the kind
     int32_t row_j[kItems][kQT][kBM];     // head of each query row, -1: none
+    int32_t q_row[kQT][kBM], kv_row[4][kBN / 4];  // rows being copied
     ChunkSplit split;
     // barriers, in the order of kBarCounts
     uint64_t item_full[kItems], rows_full[kItems], item_free[kItems];
@@ -95,14 +102,14 @@ struct Smem {
     int32_t abort_flag;
 };
 
-// Arrivals that complete a barrier: 11 readers of an item (warps 0, 1, 3 and the
-// eight softmax warps), 32 lanes of gathered K/V rows, the four warps of a
-// warpgroup, or one.
+// Arrivals that complete a barrier: the readers of an item (warps 0, 1, 3, the
+// eight softmax warps, and for gathered pages the four that copy in warp 0's place),
+// the 128 threads of those, the four warps of a warpgroup, or one.
 template <int kH, bool kGather>
 __device__ __forceinline__ uint32_t bar_count(int i) {
     constexpr int kS = Smem<kH>::kStages, kFree = 2 * kItems, kLoads = 3 * kItems, kOnes = kLoads + 2 * kS,
                   kWarps = kOnes + 2 * kS + 5 * kQT, kTail = kWarps + 4 * kQT + 3;
-    return i < kFree ? 1 : i < kLoads ? 11 : i < kOnes ? (kGather ? 32 : 1) : i < kWarps ? 1 : i < kTail ? 4 : 1;
+    return i < kFree ? 1 : i < kLoads ? (kGather ? 14 : 11) : i < kOnes ? (kGather ? 128 : 1) : i < kWarps ? 1 : i < kTail ? 4 : 1;
 }
 template <int kH>
 constexpr int bar_total() { return 3 * kItems + 4 * Smem<kH>::kStages + 9 * kQT + 5; }
@@ -433,37 +440,28 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
 }
 
 // Copies rows of 64 kH elements (of which d exist, the others zeros) to a 128-byte
-// swizzled tile, 16 bytes a lane, whole rows of adjacent lanes; lane r / 4 holds the
-// index of row r in row[r % 4], -1 for a row of zeros.
-template <int kH>
-__device__ __forceinline__ void copy_rows(uint32_t tile, const bf16* base, int64_t stride, const int (&row)[4], int rows, int d) {
+// swizzled tile, 16 bytes a lane, whole rows of adjacent lanes.  at: the rows'
+// indexes in shared memory, -1 for a row of zeros.
+template <int kH, int kUnroll>
+__device__ __forceinline__ void copy_rows(uint32_t tile, const bf16* base, int64_t stride, const int32_t* at, int rows, int d) {
     constexpr int kPer = 4 / kH;  // rows a copy
     const int lane = threadIdx.x & 31, sub = lane / (8 * kH), c = lane % (8 * kH);
-    const uint32_t dst = tile + (c >> 3) * kHalf;
+    const uint32_t dst = tile + (c >> 3) * kHalf + sub * 128;
     const bool in = kH == 2 || c * 8 < d;
-#pragma unroll 2
-    for (int j = 0; j < rows / kPer; ++j) {
-        const int r = kPer * j + sub;
-        int from;
-        if constexpr (kH == 2) {
-            const int even = __shfl_sync(0xffffffffu, (j & 1) ? row[2] : row[0], j >> 1);
-            const int odd = __shfl_sync(0xffffffffu, (j & 1) ? row[3] : row[1], j >> 1);
-            from = sub ? odd : even;
-        } else {
-            const int a = __shfl_sync(0xffffffffu, row[0], j), b = __shfl_sync(0xffffffffu, row[1], j);
-            const int e = __shfl_sync(0xffffffffu, row[2], j), f = __shfl_sync(0xffffffffu, row[3], j);
-            from = sub == 0 ? a : sub == 1 ? b : sub == 2 ? e : f;
-        }
+    const bf16* src = base + c * 8;
+#pragma unroll kUnroll
+    for (int r = 0; r < rows; r += kPer) {
+        const int from = at[r + sub];
         const bool on = from >= 0 && in;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                     "l"(base + (on ? from * stride + c * 8 : 0)), "r"(on ? 16 : 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((c & 7) ^ ((r + sub) & 7)) << 4)),
+                     "l"(on ? src + from * stride : base), "r"(on ? 16 : 0)
                      : "memory");
     }
 }
 
 // kGather: pages of fewer than 16 rows, fetched row by row.
 template <int kH, bool kGather>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Split<kGather>::kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                 const __grid_constant__ ChunkGeom u, const Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -496,7 +494,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 96) chunk_clear(u);
     tc_fence_before();
-    chunk_split<kThreads>(u, sm.split, blockIdx.x);  // with block barriers
+    chunk_split<Split<kGather>::kThreads>(u, sm.split, blockIdx.x);  // with block barriers
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     // The kinds of units this CTA has, in the order in which it runs them: every
@@ -510,9 +508,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     const int phases = has_many && has_few ? 2 : 1;
     const bool few_first = has_few && (!has_many || (blockIdx.x & 1));
 
-    if (warp == 0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (kGather && warp == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
+    } else if (kGather ? warp >= 12 : warp == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ K/V tiles
+        // (gathered: a quarter of the rows a warp; one warp has so few 16-byte copies in
+        // flight that 64 decodes ran at 1.3 TB/s)
+        const int quarter = kGather ? warp - 12 : 0;
         const int shift = u.page_shift;
         const int box_rows = shift >= 7 ? kBN : 1 << shift;
         const int boxes = kBN / box_rows;  // per tile and 64-element part
@@ -537,14 +540,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             for (int s = it.s0; s < it.s1; ++s, ++kv_it) {
                 const int st = kv_it % kStages, x0 = s * kBN;
                 const uint32_t par = ((kv_it / kStages) & 1) ^ 1;
-                int page = 0, in_page = 0, row[4];
+                int page = 0, in_page = 0;
                 if constexpr (kGather) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = it.key(x0 + lane * 4 + e);
-                        const bool on = key < it.hi && (key >= it.lo || key < u.sinks);
-                        row[e] = on ? (int)chunk_cache_row(u, it.b, key) : -1;
-                    }
+                    const int key = it.key(x0 + quarter * 32 + lane);
+                    const bool on = key < it.hi && (key >= it.lo || key < u.sinks);
+                    __syncwarp();
+                    sm.kv_row[quarter][lane] = on ? (int)chunk_cache_row(u, it.b, key) : -1;
+                    __syncwarp();
                 } else if (lane < kH * boxes) {
                     const int key = it.key(x0 + (lane / kH) * box_rows);
                     const bool on = key < it.hi && (key + box_rows > it.lo || key < u.sinks);
@@ -554,7 +556,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 }
                 auto load = [&](const CUtensorMap* map, const bf16* pages, uint64_t* bar, uint8_t* dst) {
                     if constexpr (kGather) {
-                        copy_rows<kH>(smem_u32(dst), pages + (int64_t)it.q * d, (int64_t)u.g * d, row, kBN, d);
+                        copy_rows<kH, 4>(smem_u32(dst) + quarter * 32 * 128, pages + (int64_t)it.q * d, (int64_t)u.g * d,
+                                         sm.kv_row[quarter], kBN / 4, d);
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
                     } else {
                         if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
@@ -583,7 +586,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             bar_wait(&sm.kv_full_v[i % kStages], (i / kStages) & 1);
         }
     } else if (warp == 1) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: S
         if (lane == 0) {
             const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
@@ -654,7 +657,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             bar_wait(&sm.mma_drain, 0);
         }
     } else if (warp == 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ items, row tables, Q
         // this lane's rows 4 lane .. 4 lane + 3 of a tile: token within the tile
         // (negative: none), selection
@@ -716,7 +719,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         const bool there = off >= 0 && off < it.nt, good = there && j >= it.q * u.hpg && j < (it.q + 1) * u.hpg;
                         if (there && !good) report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)(it.t0 + off));
                         sm.row_j[slot][t][lane * 4 + e] = good ? j : -1;
-                        row[t][e] = good ? (it.t0 + off) * u.h + j : -1;  // -1: zeros
+                        sm.q_row[t][lane * 4 + e] = good ? (it.t0 + off) * u.h + j : -1;
                     }
                 warp_arrive(&sm.rows_full[slot]);
 #pragma unroll
@@ -725,7 +728,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (t >= tiles) continue;
                     if (!warp_wait(sm, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
                     if (buf) ++q_fill[1]; else ++q_fill[0];
-                    copy_rows<kH>(smem_u32(sm.q[buf]), p.Q, d, row[t], few ? kFew : kBM, d);
+                    copy_rows<kH, 4>(smem_u32(sm.q[buf]), p.Q, d, sm.q_row[t], few ? kFew : kBM, d);
                     asm volatile("cp.async.commit_group;" ::: "memory");
                 }
                 if (!ok) break;
@@ -742,7 +745,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             }
         }
     } else if (warp == 3) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: O += P V
         const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
         const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v[0]), kH == 2 ? kHalf : 0);
@@ -819,7 +822,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             bar_wait(&sm.mma_drain2, 0);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsSoftmax));
         // ------------------------------------------------------------ softmax + epilogue (tile t)
         const int t = (warp - 4) >> 2;     // query tile of this warpgroup
         const int wq = warp & 3;           // TMEM lane quarter of this warp
@@ -1160,7 +1163,7 @@ namespace {
 template <int kH, bool kGather>
 bool registers_suffice() {
     cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, chunk_tc_kernel<kH, kGather>) == cudaSuccess && f.numRegs >= kRegsLaunch;
+    return cudaFuncGetAttributes(&f, chunk_tc_kernel<kH, kGather>) == cudaSuccess && f.numRegs >= Split<kGather>::kRegsLaunch;
 }
 
 template <int kH, bool kGather>
@@ -1182,7 +1185,7 @@ cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a, const CUtensorM
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(u.parts);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Split<kGather>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
