@@ -90,13 +90,13 @@ struct Smem {
     float4 wsum[kQT][kFew];              //   and their sums at the end
     ChunkItem item[kItems];
     int32_t has[kItems];                 // 0: no more items of the kind
-    int32_t row_j[kItems][kQT][kBM];     // head of each query row, -1: none
-    int32_t q_row[kQT][kBM], kv_row[4][kBN / 4];  // rows being copied
+    int32_t row[kItems][kQT][kBM];       // each query row's row of Q and O seen as [T * h, d_h], -1: none
+    int32_t kv_row[4][kBN / 4];          // cache rows being copied (gathered pages)
     ChunkSplit split;
     // barriers, in the order of kBarCounts
     uint64_t item_full[kItems], rows_full[kItems], item_free[kItems];
     uint64_t kv_full_k[kStages], kv_full_v[kStages], kv_empty_k[kStages], kv_empty_v[kStages];
-    uint64_t s_full[kQT], p_empty[kQT], o_full[kQT], q_full[kQT], q_empty[kQT], p_full[kQT], o_empty[kQT], st_free[kQT], vote[kQT];
+    uint64_t s_full[kQT], p_empty[kQT], o_full[kQT], q_full[kQT], q_empty[kQT], p_full[kQT], o_empty[kQT], st_free[kQT], vote[kQT], qm_full[kQT];
     uint64_t x_full, x_free, s_free, mma_drain, mma_drain2;
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -108,11 +108,11 @@ struct Smem {
 template <int kH, bool kGather>
 __device__ __forceinline__ uint32_t bar_count(int i) {
     constexpr int kS = Smem<kH>::kStages, kFree = 2 * kItems, kLoads = 3 * kItems, kOnes = kLoads + 2 * kS,
-                  kWarps = kOnes + 2 * kS + 5 * kQT, kTail = kWarps + 4 * kQT + 3;
+                  kWarps = kOnes + 2 * kS + 5 * kQT, kTail = kWarps + 5 * kQT + 3;
     return i < kFree ? 1 : i < kLoads ? (kGather ? 14 : 11) : i < kOnes ? (kGather ? 128 : 1) : i < kWarps ? 1 : i < kTail ? 4 : 1;
 }
 template <int kH>
-constexpr int bar_total() { return 3 * kItems + 4 * Smem<kH>::kStages + 9 * kQT + 5; }
+constexpr int bar_total() { return 3 * kItems + 4 * Smem<kH>::kStages + 10 * kQT + 5; }
 
 struct Params {
     const bf16* Q;
@@ -421,9 +421,9 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
     float check = 0.f;  // stays 0, or NaN when a value is not finite
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-        const int head = r < rows ? sm.row_j[slot][0][r] : -1;
+        const int out = r < rows ? sm.row[slot][0][r] : -1;
         const float gm = __shfl_sync(0xffffffffu, gate, r);
-        if (head < 0 || col >= d) continue;
+        if (out < 0 || col >= d) continue;
         const float v = __uint_as_float(o[r]);
         check += v * 0.f + l[r] * 0.f;
         if (partial) {
@@ -432,7 +432,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
             rec[col] = none ? 0.f : v / l[r];
             if (col == 0) rec[d] = none ? -INFINITY : m[r] + log2f(l[r]);
         } else {
-            p.O[((int64_t)(it.t0 + (r * u.inv_k >> 16)) * u.h + head) * d + col] = __float2bfloat16_rn(v * (gm / l[r]));
+            p.O[(int64_t)out * d + col] = __float2bfloat16_rn(v * (gm / l[r]));
         }
     }
     if (!(check == 0.f) && !partial) u.odd[u.parts + blockIdx.x] = 1;
@@ -598,7 +598,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             auto s_buffer = [&]() { return s_cnt == 0 || bar_wait(&sm.s_free, (s_cnt - 1) & 1); };
             auto st_buffer = [&](int t) { return st_cnt[t] == 0 || bar_wait(&sm.st_free[t], (st_cnt[t] - 1) & 1); };
             bool few = few_first;
-            uint32_t q_use[kQT] = {0, 0}, few_it = 0;  // fills of the Q buffers so far; few-row items
+            uint32_t q_use[kQT] = {0, 0}, qm_use[kQT] = {0, 0}, few_it = 0;  // fills of the Q buffers so far; few-row items
     #pragma unroll 1
         for (int ui = 0, ends = 0; ok && !aborted(sm); ++ui) {
                 const int slot = ui % kItems;
@@ -613,13 +613,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const int n0 = tile_steps(u, sm.item[slot], 0, few), n1 = tile_steps(u, sm.item[slot], 1, few);
                 const int tiles = sm.item[slot].nt > u.W ? 2 : 1;
                 mbar_arrive(&sm.item_free[slot]);
-                // Q: few rows, the buffers in turn; many, one per tile
+                // Q: few rows, the buffers in turn, filled by warp 2; many, one per tile,
+                // filled by the tile's softmax warps
                 const int qb = few ? few_it++ & 1 : 0;
                 const uint32_t q_lo = qb ? q_lo1 : q_lo0;
                 for (int t = 0; t < kQT && ok; ++t) {
                     if (few ? t != qb : t > 0 && tiles < 2) continue;
-                    ok = bar_wait(&sm.q_full[t], (t ? q_use[1] : q_use[0]) & 1);
-                    if (t) ++q_use[1]; else ++q_use[0];
+                    if (few) {
+                        ok = bar_wait(&sm.q_full[t], (t ? q_use[1] : q_use[0]) & 1);
+                        if (t) ++q_use[1]; else ++q_use[0];
+                    } else {
+                        ok = bar_wait(&sm.qm_full[t], (t ? qm_use[1] : qm_use[0]) & 1);
+                        if (t) ++qm_use[1]; else ++qm_use[0];
+                    }
                 }
                 if (!ok) { fail(sm, 11); break; }
                 if (few ? !s_buffer() : !(st_buffer(0) && st_buffer(1))) { fail(sm, 14); break; }
@@ -690,7 +696,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     ++ui;
                     break;
                 }
-                const int tiles = it.nt > u.W ? 2 : 1, qb = few ? few_it++ & 1 : 0;
+                const int tiles = it.nt > u.W ? 2 : 1;
                 int row[kQT][4];  // the lane's rows of Q
 #pragma unroll
                 for (int t = 0; t < kQT; ++t)
@@ -707,10 +713,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     }
                     __syncwarp();
                 };
-                // Many rows: the first item's K/V loads queue up behind its Q rows, not
-                // before them; else they need not wait for the Q buffers to be free.
-                const bool early = few || ui > 0;
-                if (early) publish();
+                if (lane == 0) {
+                    sm.has[slot] = 1;
+                    sm.item[slot] = it;
+                    mbar_arrive(&sm.item_full[slot]);
+                }
+                __syncwarp();
 #pragma unroll
                 for (int t = 0; t < kQT; ++t)
 #pragma unroll
@@ -718,30 +726,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         const int off = tok[e] + t * u.W, j = row[t][e];
                         const bool there = off >= 0 && off < it.nt, good = there && j >= it.q * u.hpg && j < (it.q + 1) * u.hpg;
                         if (there && !good) report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)(it.t0 + off));
-                        sm.row_j[slot][t][lane * 4 + e] = good ? j : -1;
-                        sm.q_row[t][lane * 4 + e] = good ? (it.t0 + off) * u.h + j : -1;
+                        sm.row[slot][t][lane * 4 + e] = good ? (it.t0 + off) * u.h + j : -1;
                     }
                 warp_arrive(&sm.rows_full[slot]);
-#pragma unroll
-                for (int t = 0; t < kQT; ++t) {
-                    const int buf = few ? qb : t;
-                    if (t >= tiles) continue;
-                    if (!warp_wait(sm, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
-                    if (buf) ++q_fill[1]; else ++q_fill[0];
-                    copy_rows<kH, 4>(smem_u32(sm.q[buf]), p.Q, d, sm.q_row[t], few ? kFew : kBM, d);
-                    asm volatile("cp.async.commit_group;" ::: "memory");
+                if (!few) {  // the softmax warps copy the tiles
+                    ++q_fill[0];
+                    if (tiles == 2) ++q_fill[1];
+                    continue;
                 }
-                if (!ok) break;
-                if (!early) publish();
-                // each tile as it lands, from the generic to the tensor cores' view
-                if (tiles == 2) {
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    fence_proxy_async_smem();
-                    warp_arrive(&sm.q_full[0]);
-                }
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-                fence_proxy_async_smem();
-                warp_arrive(&sm.q_full[few ? qb : tiles - 1]);
+                const int buf = few_it++ & 1;
+                if (!warp_wait(sm, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
+                if (buf) ++q_fill[1]; else ++q_fill[0];
+                copy_rows<kH, 4>(smem_u32(sm.q[buf]), p.Q, d, sm.row[slot][0], kFew, d);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();  // from the generic to the tensor cores' view
+                warp_arrive(&sm.q_full[buf]);
             }
         }
     } else if (warp == 3) {
@@ -835,7 +834,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const int sel = r - (r * u.inv_k >> 16) * u.k;
         const bool in_tile = r < u.W * u.k;
         const uint64_t C2 = pk2(p.scale_log2, p.scale_log2);
-        uint32_t ctile = 0, o_it = 0, votes = 0, swaps = 0;
+        uint32_t ctile = 0, o_it = 0, votes = 0, swaps = 0, few_items = 0;
         uint32_t ui = 0;
         // The next item of the kind, or null at its end (or after a failure).
         auto take = [&]() -> const ChunkItem* {
@@ -850,15 +849,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         // a token taking its slots in turn.
         auto zero_fill = [&](const ChunkItem& it, int toks) {
             if (it.s0 != 0 || u.k == u.hpg || r >= toks * u.k) return;
-            const int32_t* heads = sm.row_j[ui % kItems][t] + (r - sel);
-            bf16* o = p.O + ((int64_t)(it.t0 + off) * u.h + it.q * u.hpg) * d;
+            const int32_t* rows = sm.row[ui % kItems][t] + (r - sel);
+            const int first = (it.t0 + off) * u.h + it.q * u.hpg;
+            bf16* o = p.O + (int64_t)first * d;
             int turn = 0;
 #pragma unroll 1
             for (int a0 = 0; a0 < u.hpg; a0 += 32) {
                 uint32_t free = low_bits(u.hpg - a0);
 #pragma unroll 1
                 for (int a = 0; a < u.k; ++a) {
-                    const int j = heads[a] - it.q * u.hpg - a0;
+                    const int j = rows[a] - first - a0;
                     if (j >= 0 && j < 32) free &= ~(1u << j);
                 }
 #pragma unroll 1
@@ -880,16 +880,31 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const ChunkItem it = *next;
                 const int slot = ui % kItems;
                 if (!warp_wait(sm, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
+                ++few_items;
                 if (t == 0) zero_fill(it, it.nt);
                 if (!(it.nt * u.k <= 4 ? few_item<4, kH>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)
                                        : few_item<16, kH>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)))
                     break;
                 done();
             }
-            // group 0 has read what group 1 handed over: x is the stages' now
+            if (phase + 1 == phases) continue;
+            // The last few-row items' products have read the Q buffer that the many
+            // rows' tile t takes, and group 0 has read what group 1 handed over: x is
+            // the stages' now.
+            if (few_items > t && !aborted(sm)) warp_wait(sm, &sm.q_empty[t], ((few_items - t + 1) / 2 - 1) & 1, 53);
             if (swaps > 0 && !aborted(sm)) warp_wait(sm, &sm.x_free, (swaps - 1) & 1, 52);
             continue;
         }
+        // This warp's rows of an item's Q tile, in flight until q_ready.
+        auto load_q = [&](int slot) {
+            copy_rows<kH, 4>(smem_u32(sm.q[t]) + wq * 32 * 128, p.Q, d, sm.row[slot][t] + wq * 32, 32, d);
+        };
+        auto q_ready = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();  // from the generic to the tensor cores' view
+            warp_arrive(&sm.qm_full[t]);
+        };
+        bool loaded = false;  // the next item's Q tile is on its way already
         while (const ChunkItem* next = take()) {
             const ChunkItem& it = *next;  // read again where it is used: registers are short in the loop
             const int slot = ui % kItems;
@@ -902,12 +917,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 done();
                 continue;
             }
+            if (!loaded) load_q(slot);
+            q_ready();
+            loaded = false;
             const bool partial = it.rec >= 0;
             const bool mine = in_tile && off < it.nt;
             const int token = it.t0 + off;
             const float gate = mine ? u.gate[((int64_t)token * u.g + it.q) * u.k + sel] : 0.f;
             zero_fill(it, toks);
-            const int head = mine ? sm.row_j[slot][t][r] : -1;
+            const int out_row = mine ? sm.row[slot][t][r] : -1;
             const bool live = wq * 32 < toks * u.k;  // some row of this warp is a query row
             // Keys this row sees: [low, pos] and those below u.sinks.  A padding row
             // sees all (its result is dropped).
@@ -1046,6 +1064,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 }
             }
             if (!ok) break;
+            // The tile's last S is done: its Q buffer takes the next item's rows while
+            // this one's epilogue runs.
+            {
+                const int ns = (ui + 1) % kItems;
+                if (!warp_wait(sm, &sm.item_full[ns], ((ui + 1) / kItems) & 1, 54)) break;
+                if (sm.has[ns] && sm.item[ns].nt > t * u.W) {
+                    if (!warp_wait(sm, &sm.rows_full[ns], ((ui + 1) / kItems) & 1, 55)) break;
+                    load_q(ns);
+                    loaded = true;
+                }
+            }
             // Epilogue: O_t / l, gated, as the bf16 row of O, or the row's partial
             // record (o, log2-sum-exp); none of this part's keys seen: -inf.  A row per
             // thread would store 16 bytes to each of 32 lines at a time, so 64 bytes of
@@ -1079,14 +1108,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             for (int cb = 0; cb < 2 * kH; ++cb)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) check[e & 3] = fmaf(__uint_as_float(o[cb][e]), 0.f, check[e & 3]);
-            if (head >= 0) {
+            if (out_row >= 0) {
                 if (!partial && !((check[0] + check[1]) + (check[2] + check[3]) == 0.f)) u.odd[blockIdx.x] = 1;
                 if (partial) u.part[(int64_t)(rec_row + lane) * (d + 4) + d] = none ? -INFINITY : m + log2f(l);
             }
             uint4* stage = sm.stage(t, wq);
             // This lane's 16 bytes of four of the warp's rows: 8 e + lane / 4.
             uint4* to[4];
-            const int out_row = head >= 0 ? token * u.h + head : -1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int row = 8 * e + (lane >> 2), there = __shfl_sync(0xffffffffu, out_row, row);
