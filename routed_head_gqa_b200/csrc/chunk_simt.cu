@@ -6,8 +6,8 @@
 // running row maximum and sum (S = Q K^T, P = 2^(S c - m), O += P V, rescaled
 // when the maximum grows).  256 threads as 16 x 16: thread (ty, tx) holds rows
 // ty + 16 i and keys tx + 16 j of S, and rows ty + 16 i of O, so a row's P is
-// written and read by one half warp.  A unit of at most 16 rows (a decode)
-// computes one row per thread instead of four.  K and V have one buffer each:
+// written and read by one half warp.  A unit of at most 16 rows computes one row
+// per thread instead of four, one of at most 4 (a decode) goes by run_few.  K and V have one buffer each:
 // the copy of the next K runs under the softmax and P V, that of the next V under
 // the next S.
 #include "chunk.cuh"
@@ -85,7 +85,22 @@ struct SimtShared {
     ChunkItem item;
     int has;
     int row_j[kBM];
+    float wmax[4][kThreads / 32];  // few rows: the warps' maxima, then their sums
 };
+
+// The unit's unselected output slots, by the part that holds its first step.
+template <typename T, int D>
+__device__ __forceinline__ void zero_unselected(const ChunkGeom& u, const ChunkItem& it, const SimtShared& sh, T* O) {
+    if (it.s0 != 0) return;
+    constexpr int kVec = 16 / sizeof(T), kPer = D / kVec;
+    for (int v = threadIdx.x; v < it.nt * u.hpg * kPer; v += kThreads) {
+        const int x = v % kPer, j = it.q * u.hpg + (v / kPer) % u.hpg, i = v / kPer / u.hpg;
+        bool chosen = false;
+        for (int r = 0; r < u.k; ++r) chosen |= sh.row_j[i * u.k + r] == j;
+        if (!chosen)
+            *reinterpret_cast<uint4*>(O + ((int64_t)(it.t0 + i) * u.h + j) * D + x * kVec) = make_uint4(0, 0, 0, 0);
+    }
+}
 
 template <typename T, int D, int NR>
 __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it, const SimtShared& sh, const T* Q,
@@ -116,17 +131,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
         for (int e = 0; e < kVec; e += 4)
             *reinterpret_cast<float4*>(Qs + r * C::kQ + x + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
     }
-    // the unit's unselected output slots, by the part that holds its first step
-    if (it.s0 == 0) {
-        constexpr int kPer = D / kVec;
-        for (int v = tid; v < it.nt * u.hpg * kPer; v += kThreads) {
-            const int x = v % kPer, j = it.q * u.hpg + (v / kPer) % u.hpg, i = v / kPer / u.hpg;
-            bool chosen = false;
-            for (int r = 0; r < u.k; ++r) chosen |= sh.row_j[i * u.k + r] == j;
-            if (!chosen)
-                *reinterpret_cast<uint4*>(O + ((int64_t)(it.t0 + i) * u.h + j) * D + x * kVec) = make_uint4(0, 0, 0, 0);
-        }
-    }
+    zero_unselected<T, D>(u, it, sh, O);
 
     float m[NR], l[NR], acc[NR][kCols];
     int pos[NR];
@@ -262,6 +267,137 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
     }
 }
 
+// Few rows (a decode): the 16 x 16 threads over rows and keys would compute 16 rows
+// for 1 to 4.  Scores: four threads a key, a quarter of the head each.  P V: a thread
+// per element of the head and kThreads / D groups of keys, joined at the end.  The
+// running maximum is the tile's for all threads, from shared memory.
+template <typename T, int D, int R>
+__device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it, SimtShared& sh, const T* Q, const T* Kp,
+                                        const T* Vp, T* O, float scale_log2, float* Qs, float* Ps, T* Ks, T* Vs) {
+    using C = SimtCfg<T, D>;
+    constexpr int kVec = C::kVec, kGroups = kThreads / D, kKeys = kBN / kGroups, kQuarter = D / 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, key = tid >> 2, part = tid & 3;
+    const int col = tid % D, grp = tid / D;
+    const int rows = it.nt * u.k;
+    load_tile<T, D>(u, it, it.s0, Kp, Ks);
+    cp_async_commit();
+    load_tile<T, D>(u, it, it.s0, Vp, Vs);
+    cp_async_commit();
+    for (int x = tid; x < R * D; x += kThreads) {
+        const int r = x / D, c = x % D;
+        float q = 0.f;
+        if (r < rows && sh.row_j[r] >= 0)
+            q = Elem<T>::to_f(Q[((int64_t)(it.t0 + r / u.k) * u.h + sh.row_j[r]) * D + c]);
+        Qs[r * C::kQ + c] = q;
+    }
+    zero_unselected<T, D>(u, it, sh, O);
+    float m[R], l[R], acc[R];
+    int pos[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = acc[r] = 0.f;
+        pos[r] = r < rows ? it.p0 + r / u.k : -1;
+    }
+    for (int st = it.s0; st < it.s1; ++st) {
+        cp_async_wait<1>();
+        __syncthreads();
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r] = 0.f;
+#pragma unroll
+        for (int x = 0; x < kQuarter; x += kVec) {
+            // quarters interleaved by 16 bytes, so that four threads read 64 adjacent ones
+            const int at = x * 4 + part * kVec;
+            float kf[kVec];
+            unpack16(*reinterpret_cast<const uint4*>(Ks + key * C::kKV + at), kf, (const T*)nullptr);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) s[r] = fmaf(Qs[r * C::kQ + at + e], kf[e], s[r]);
+        }
+        const int abs_key = it.key(st * kBN + key);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+            s[r] = chunk_sees(u, pos[r], abs_key) ? s[r] * scale_log2 : -INFINITY;
+            float mx = s[r];
+#pragma unroll
+            for (int d = 16; d >= 4; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            if (lane == 0) sh.wmax[r][warp] = mx;
+        }
+        __syncthreads();  // K read, maxima written
+        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Kp, Ks);
+        cp_async_commit();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float mx = m[r];
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) mx = fmaxf(mx, sh.wmax[r][w]);
+            const float ref = mx == -INFINITY ? 0.f : mx, corr = fast_exp2(m[r] - ref);
+            m[r] = mx;
+            const float w = fast_exp2(s[r] - ref);
+            l[r] = l[r] * corr + (part == 0 ? w : 0.f);  // this thread's keys; summed at the end
+            acc[r] *= corr;
+            if (part == 0) Ps[r * kPStride + key] = w;
+        }
+        cp_async_wait<1>();
+        __syncthreads();  // V here, P written
+#pragma unroll
+        for (int k0 = 0; k0 < kKeys; k0 += 4) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = Elem<T>::to_f(Vs[(grp * kKeys + k0 + e) * C::kKV + col]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 w = *reinterpret_cast<const float4*>(Ps + r * kPStride + grp * kKeys + k0);
+                acc[r] = fmaf(w.x, v[0], acc[r]);
+                acc[r] = fmaf(w.y, v[1], acc[r]);
+                acc[r] = fmaf(w.z, v[2], acc[r]);
+                acc[r] = fmaf(w.w, v[3], acc[r]);
+            }
+        }
+        __syncthreads();  // V and P read
+        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Vp, Vs);
+        cp_async_commit();
+    }
+    // join the groups of keys (in the tile of P) and the threads' sums
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float sum = l[r];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) sh.wmax[r][warp] = sum;
+        Ps[r * kThreads + tid] = acc[r];
+    }
+    __syncthreads();
+    const bool partial = it.rec >= 0;
+    for (int x = tid; x < rows * D; x += kThreads) {
+        const int r = x / D, c = x % D, j = sh.row_j[r];
+        if (j < 0) continue;
+        float sum = 0.f, o = 0.f, mr = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) sum += sh.wmax[r][w];
+#pragma unroll
+        for (int g2 = 0; g2 < kGroups; ++g2) o += Ps[r * kThreads + g2 * D + c];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i == r) mr = m[i];
+        const bool none = mr == -INFINITY && sum == 0.f;
+        const int token = it.t0 + r / u.k;
+        if (partial) {
+            float* rec = u.part + (int64_t)(it.rec + r) * (D + 4);
+            rec[c] = none ? 0.f : o / sum;
+            if (c == 0) rec[D] = none ? -INFINITY : mr + log2f(sum);
+        } else {
+            if (!(o * 0.f + sum * 0.f == 0.f)) u.odd[blockIdx.x] = 1;
+            O[((int64_t)token * u.h + j) * D + c] =
+                Elem<T>::from_f(o * (u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] / sum));
+        }
+    }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
@@ -294,7 +430,11 @@ chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, 
         const int rows = it.nt * u.k;
         for (int r = tid; r < rows; r += kThreads) sh.row_j[r] = chunk_head(u, it.t0 + r / u.k, it.q, r % u.k);
         __syncthreads();
-        if (rows <= 16)
+        if (rows <= 2)
+            run_few<T, D, 2>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+        else if (rows <= 4)
+            run_few<T, D, 4>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+        else if (rows <= 16)
             run_item<T, D, 1>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
         else
             run_item<T, D, 4>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
@@ -303,8 +443,9 @@ chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, 
     cp_async_wait<0>();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a) {
+    using T = float;
     const size_t smem = SimtCfg<T, D>::kSmem;
     cudaError_t err = cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
@@ -316,14 +457,13 @@ cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a) {
 
 }  // namespace
 
-ChunkTiling chunk_simt_tiling() { return {kBM, 1, 0, kBN, 2 * kBN, 0, 4 * kBN, 2}; }
+ChunkTiling chunk_simt_tiling() { return {kBM, 1, 0, kBN, kBN, 0, kBN, 1}; }
 
 cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a) {
-    const bool bf = a.s->dtype == GQE_BF16;
     switch (a.s->d_h) {
-        case 32: return bf ? launch_typed<__nv_bfloat16, 32>(u, a) : launch_typed<float, 32>(u, a);
-        case 64: return bf ? launch_typed<__nv_bfloat16, 64>(u, a) : launch_typed<float, 64>(u, a);
-        case 128: return bf ? launch_typed<__nv_bfloat16, 128>(u, a) : launch_typed<float, 128>(u, a);
+        case 32: return launch_typed<32>(u, a);
+        case 64: return launch_typed<64>(u, a);
+        case 128: return launch_typed<128>(u, a);
         default: return cudaErrorInvalidValue;
     }
 }
