@@ -1,15 +1,19 @@
 // chunk_simt.cu -- routed attention of ragged chunks of new tokens over a paged
-// cache on the CUDA cores (every type and head width).  See chunk.cuh for the
-// units and the schedule.
+// cache on the CUDA cores, for fp32 caches (d_h = 128, 64 or 32).  See chunk.cuh for
+// the units and the schedule.
 //
 // Per unit: up to 64 query rows, 64 keys a step, one pass over the keys with the
 // running row maximum and sum (S = Q K^T, P = 2^(S c - m), O += P V, rescaled
-// when the maximum grows).  256 threads as 16 x 16: thread (ty, tx) holds rows
-// ty + 16 i and keys tx + 16 j of S, and rows ty + 16 i of O, so a row's P is
-// written and read by one half warp.  A unit of at most 16 rows computes one row
-// per thread instead of four, one of at most 4 (a decode) goes by run_few.  K and V have one buffer each:
-// the copy of the next K runs under the softmax and P V, that of the next V under
-// the next S.
+// when the maximum grows), all in fp32.  256 threads as 16 x 16: thread (ty, tx)
+// holds rows ty + 16 i and keys tx + 16 j of S, and rows ty + 16 i of O, so a row's
+// P is written and read by one half warp.  K and V have one buffer each: the copy of
+// the next K runs under the softmax and P V, that of the next V under the next S.
+//
+// Three forms by the unit's rows.  Up to 4 (a decode): run_few, since the 16 x 16
+// threads would compute 16 rows (16 decodes, d_h = 128, 158 us against 301).  Up to
+// 16: one row per thread.  Above: four.  Bound by the fp32 pipes and shared memory
+// (four loads of Q and four of K feed 64 products per thread): 20 TFLOP/s at
+// d_h = 128 over a prompt, 2.1 TB/s over decodes.
 #include "chunk.cuh"
 
 namespace gqe {
@@ -18,12 +22,12 @@ namespace {
 constexpr int kBM = 64, kBN = 64, kThreads = 256;
 constexpr int kPStride = kBN + 4;
 
-template <typename T, int D>
+template <int D>
 struct SimtCfg {
-    static constexpr int kVec = 16 / sizeof(T);           // elements per 16 bytes
+    static constexpr int kVec = 16 / sizeof(float);           // elements per 16 bytes
     static constexpr int kKV = D + kVec;                  // K/V row stride: rows 16 bytes apart modulo the banks
     static constexpr int kQ = D + 4;
-    static constexpr size_t kSmem = sizeof(float) * (kBM * kQ + kBM * kPStride) + 2 * sizeof(T) * kBN * kKV;
+    static constexpr size_t kSmem = sizeof(float) * (kBM * kQ + kBM * kPStride) + 2 * sizeof(float) * kBN * kKV;
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
@@ -36,14 +40,14 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // One tile of K or V rows; keys that no row of the unit sees are zeros.
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(const ChunkGeom& u, const ChunkItem& it, int step, const T* pages, T* dst) {
-    using C = SimtCfg<T, D>;
+template <int D>
+__device__ __forceinline__ void load_tile(const ChunkGeom& u, const ChunkItem& it, int step, const float* pages, float* dst) {
+    using C = SimtCfg<D>;
     constexpr int kPer = D / C::kVec;  // 16-byte vectors per row
     for (int v = threadIdx.x; v < kBN * kPer; v += kThreads) {
         const int row = v / kPer, x = (v % kPer) * C::kVec, s = it.key(step * kBN + row);
         const bool on = s < it.hi && (s >= it.lo || s < u.sinks);
-        const T* src = pages;
+        const float* src = pages;
         if (on) src += (chunk_cache_row(u, it.b, s) * u.g + it.q) * D + x;
         cp_async16(dst + row * C::kKV + x, src, on);
     }
@@ -58,28 +62,12 @@ __device__ __forceinline__ void load_cols(const float* p, float (&f)[2]) {
     const float2 v = *reinterpret_cast<const float2*>(p);
     f[0] = v.x, f[1] = v.y;
 }
-__device__ __forceinline__ void load_cols(const __nv_bfloat16* p, float (&f)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load_cols(const __nv_bfloat16* p, float (&f)[2]) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-    f[0] = __uint_as_float(v << 16), f[1] = __uint_as_float(v & 0xffff0000u);
-}
 __device__ __forceinline__ void store_cols(float* p, const float (&f)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
 __device__ __forceinline__ void store_cols(float* p, const float (&f)[2]) {
     *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
 }
-__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&f)[4]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&f)[2]) {
-    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
-}
-
 struct SimtShared {
     ChunkSplit split;
     ChunkItem item;
@@ -89,10 +77,10 @@ struct SimtShared {
 };
 
 // The unit's unselected output slots, by the part that holds its first step.
-template <typename T, int D>
-__device__ __forceinline__ void zero_unselected(const ChunkGeom& u, const ChunkItem& it, const SimtShared& sh, T* O) {
+template <int D>
+__device__ __forceinline__ void zero_unselected(const ChunkGeom& u, const ChunkItem& it, const SimtShared& sh, float* O) {
     if (it.s0 != 0) return;
-    constexpr int kVec = 16 / sizeof(T), kPer = D / kVec;
+    constexpr int kVec = 16 / sizeof(float), kPer = D / kVec;
     for (int v = threadIdx.x; v < it.nt * u.hpg * kPer; v += kThreads) {
         const int x = v % kPer, j = it.q * u.hpg + (v / kPer) % u.hpg, i = v / kPer / u.hpg;
         bool chosen = false;
@@ -102,19 +90,19 @@ __device__ __forceinline__ void zero_unselected(const ChunkGeom& u, const ChunkI
     }
 }
 
-template <typename T, int D, int NR>
-__device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it, const SimtShared& sh, const T* Q,
-                                         const T* Kp, const T* Vp, T* O, float scale_log2, float* Qs, float* Ps, T* Ks,
-                                         T* Vs) {
-    using C = SimtCfg<T, D>;
+template <int D, int NR>
+__device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it, const SimtShared& sh, const float* Q,
+                                         const float* Kp, const float* Vp, float* O, float scale_log2, float* Qs, float* Ps, float* Ks,
+                                         float* Vs) {
+    using C = SimtCfg<D>;
     constexpr int kVec = C::kVec;
     constexpr int kCols = D / 16, kCW = kCols < 4 ? kCols : 4, kCN = kCols / kCW;  // O columns per thread
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rows = it.nt * u.k;
 
-    load_tile<T, D>(u, it, it.s0, Kp, Ks);
+    load_tile<D>(u, it, it.s0, Kp, Ks);
     cp_async_commit();
-    load_tile<T, D>(u, it, it.s0, Vp, Vs);
+    load_tile<D>(u, it, it.s0, Vp, Vs);
     cp_async_commit();
     // Q rows as fp32 (rows past the unit's, or of a bad selection, as zeros)
     for (int v = tid; v < NR * 16 * (D / kVec); v += kThreads) {
@@ -122,7 +110,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
         float f[kVec];
         if (r < rows && sh.row_j[r] >= 0) {
             const int token = it.t0 + r / u.k;
-            unpack16(*reinterpret_cast<const uint4*>(Q + ((int64_t)token * u.h + sh.row_j[r]) * D + x), f, (const T*)nullptr);
+            load_cols(Q + ((int64_t)token * u.h + sh.row_j[r]) * D + x, f);
         } else {
 #pragma unroll
             for (int e = 0; e < kVec; ++e) f[e] = 0.f;
@@ -131,7 +119,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
         for (int e = 0; e < kVec; e += 4)
             *reinterpret_cast<float4*>(Qs + r * C::kQ + x + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
     }
-    zero_unselected<T, D>(u, it, sh, O);
+    zero_unselected<D>(u, it, sh, O);
 
     float m[NR], l[NR], acc[NR][kCols];
     int pos[NR];
@@ -158,7 +146,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
             float kf[4][kVec];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                unpack16(*reinterpret_cast<const uint4*>(Ks + (tx + 16 * j) * C::kKV + x), kf[j], (const T*)nullptr);
+                load_cols(Ks + (tx + 16 * j) * C::kKV + x, kf[j]);
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
 #pragma unroll
@@ -175,7 +163,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
             }
         }
         __syncthreads();  // every thread has read K
-        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Kp, Ks);
+        if (st + 1 < it.s1) load_tile<D>(u, it, st + 1, Kp, Ks);
         cp_async_commit();
         int key[4];
 #pragma unroll
@@ -228,7 +216,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
             }
         }
         __syncthreads();  // every thread has read V
-        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Vp, Vs);
+        if (st + 1 < it.s1) load_tile<D>(u, it, st + 1, Vp, Vs);
         cp_async_commit();
     }
 
@@ -249,7 +237,7 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
         if (j >= 0) {
             const int token = it.t0 + r / u.k;
             float* rec = partial ? u.part + (int64_t)(it.rec + r) * (D + 4) : nullptr;
-            T* o = O + ((int64_t)token * u.h + j) * D;
+            float* o = O + ((int64_t)token * u.h + j) * D;
             const float f = partial ? inv : u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] * inv;
 #pragma unroll
             for (int cn = 0; cn < kCN; ++cn) {
@@ -271,26 +259,25 @@ __device__ __forceinline__ void run_item(const ChunkGeom& u, const ChunkItem& it
 // for 1 to 4.  Scores: four threads a key, a quarter of the head each.  P V: a thread
 // per element of the head and kThreads / D groups of keys, joined at the end.  The
 // running maximum is the tile's for all threads, from shared memory.
-template <typename T, int D, int R>
-__device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it, SimtShared& sh, const T* Q, const T* Kp,
-                                        const T* Vp, T* O, float scale_log2, float* Qs, float* Ps, T* Ks, T* Vs) {
-    using C = SimtCfg<T, D>;
+template <int D, int R>
+__device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it, SimtShared& sh, const float* Q, const float* Kp,
+                                        const float* Vp, float* O, float scale_log2, float* Qs, float* Ps, float* Ks, float* Vs) {
+    using C = SimtCfg<D>;
     constexpr int kVec = C::kVec, kGroups = kThreads / D, kKeys = kBN / kGroups, kQuarter = D / 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, key = tid >> 2, part = tid & 3;
     const int col = tid % D, grp = tid / D;
     const int rows = it.nt * u.k;
-    load_tile<T, D>(u, it, it.s0, Kp, Ks);
+    load_tile<D>(u, it, it.s0, Kp, Ks);
     cp_async_commit();
-    load_tile<T, D>(u, it, it.s0, Vp, Vs);
+    load_tile<D>(u, it, it.s0, Vp, Vs);
     cp_async_commit();
     for (int x = tid; x < R * D; x += kThreads) {
         const int r = x / D, c = x % D;
         float q = 0.f;
-        if (r < rows && sh.row_j[r] >= 0)
-            q = Elem<T>::to_f(Q[((int64_t)(it.t0 + r / u.k) * u.h + sh.row_j[r]) * D + c]);
+        if (r < rows && sh.row_j[r] >= 0) q = Q[((int64_t)(it.t0 + r / u.k) * u.h + sh.row_j[r]) * D + c];
         Qs[r * C::kQ + c] = q;
     }
-    zero_unselected<T, D>(u, it, sh, O);
+    zero_unselected<D>(u, it, sh, O);
     float m[R], l[R], acc[R];
     int pos[R];
 #pragma unroll
@@ -310,7 +297,7 @@ __device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it,
             // quarters interleaved by 16 bytes, so that four threads read 64 adjacent ones
             const int at = x * 4 + part * kVec;
             float kf[kVec];
-            unpack16(*reinterpret_cast<const uint4*>(Ks + key * C::kKV + at), kf, (const T*)nullptr);
+            load_cols(Ks + key * C::kKV + at, kf);
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -328,7 +315,7 @@ __device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it,
             if (lane == 0) sh.wmax[r][warp] = mx;
         }
         __syncthreads();  // K read, maxima written
-        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Kp, Ks);
+        if (st + 1 < it.s1) load_tile<D>(u, it, st + 1, Kp, Ks);
         cp_async_commit();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -348,7 +335,7 @@ __device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it,
         for (int k0 = 0; k0 < kKeys; k0 += 4) {
             float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = Elem<T>::to_f(Vs[(grp * kKeys + k0 + e) * C::kKV + col]);
+            for (int e = 0; e < 4; ++e) v[e] = Vs[(grp * kKeys + k0 + e) * C::kKV + col];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float4 w = *reinterpret_cast<const float4*>(Ps + r * kPStride + grp * kKeys + k0);
@@ -359,7 +346,7 @@ __device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it,
             }
         }
         __syncthreads();  // V and P read
-        if (st + 1 < it.s1) load_tile<T, D>(u, it, st + 1, Vp, Vs);
+        if (st + 1 < it.s1) load_tile<D>(u, it, st + 1, Vp, Vs);
         cp_async_commit();
     }
     // join the groups of keys (in the tile of P) and the threads' sums
@@ -393,22 +380,22 @@ __device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it,
         } else {
             if (!(o * 0.f + sum * 0.f == 0.f)) u.odd[blockIdx.x] = 1;
             O[((int64_t)token * u.h + j) * D + c] =
-                Elem<T>::from_f(o * (u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] / sum));
+                o * (u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] / sum);
         }
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
-                  T* __restrict__ O, float scale_log2) {
-    using C = SimtCfg<T, D>;
+chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const float* __restrict__ Q, const float* __restrict__ Kp, const float* __restrict__ Vp,
+                  float* __restrict__ O, float scale_log2) {
+    using C = SimtCfg<D>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ SimtShared sh;
     float* Qs = reinterpret_cast<float*>(smem);
     float* Ps = Qs + kBM * C::kQ;
-    T* Ks = reinterpret_cast<T*>(Ps + kBM * kPStride);
-    T* Vs = Ks + kBN * C::kKV;
+    float* Ks = Ps + kBM * kPStride;
+    float* Vs = Ks + kBN * C::kKV;
     const int tid = threadIdx.x;
 
     if (tid == 0) chunk_clear(u);
@@ -431,13 +418,13 @@ chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, 
         for (int r = tid; r < rows; r += kThreads) sh.row_j[r] = chunk_head(u, it.t0 + r / u.k, it.q, r % u.k);
         __syncthreads();
         if (rows <= 2)
-            run_few<T, D, 2>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+            run_few<D, 2>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
         else if (rows <= 4)
-            run_few<T, D, 4>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+            run_few<D, 4>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
         else if (rows <= 16)
-            run_item<T, D, 1>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+            run_item<D, 1>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
         else
-            run_item<T, D, 4>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
+            run_item<D, 4>(u, it, sh, Q, Kp, Vp, O, scale_log2, Qs, Ps, Ks, Vs);
         __syncthreads();  // the item, its row table and tiles may be overwritten
     }
     cp_async_wait<0>();
@@ -445,13 +432,12 @@ chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, 
 
 template <int D>
 cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a) {
-    using T = float;
-    const size_t smem = SimtCfg<T, D>::kSmem;
-    cudaError_t err = cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = SimtCfg<D>::kSmem;
+    cudaError_t err = cudaFuncSetAttribute(chunk_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-    chunk_simt_kernel<T, D><<<u.parts, kThreads, smem, a.stream>>>(u, (const T*)a.Q, (const T*)a.K_pages,
-                                                                 (const T*)a.V_pages, (T*)a.O, scale_log2);
+    chunk_simt_kernel<D><<<u.parts, kThreads, smem, a.stream>>>(u, (const float*)a.Q, (const float*)a.K_pages,
+                                                                 (const float*)a.V_pages, (float*)a.O, scale_log2);
     return cudaGetLastError();
 }
 
