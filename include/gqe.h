@@ -571,7 +571,7 @@ gqe_status gqe_kv_append(const gqe_shape* s, const void* K_new, int64_t k_stride
  * that the window has left may be stale.  Infinities and NaN in keys or values
  * that a row does not see, and rows past a cache's length, do not reach it.
  * The result is the same in every run (no atomics on values).
- * Implemented cases: bf16 or fp32, d_h in {32, 64, 128}.
+ * Implemented cases: bf16 or fp32, d_h in {32, 64, 128}, T * h < 2^31 - 1.
  */
 size_t gqe_chunk_workspace_bytes(const gqe_shape* s);
 gqe_status gqe_attn_chunk_paged(const gqe_shape* s, const void* Q, const void* K_pages, const void* V_pages,

@@ -501,6 +501,7 @@ gqe_status gqe_attn_chunk_paged(const gqe_shape* s, const void* Q, const void* K
         return GQE_ERR_INVALID_ARGUMENT;
     if (!aligned16(Q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(O)) return GQE_ERR_INVALID_ARGUMENT;
     if (s->d_h != 32 && s->d_h != 64 && s->d_h != 128) return GQE_ERR_UNSUPPORTED;
+    if ((int64_t)s->T * s->h >= ((int64_t)1 << 31) - 1) return GQE_ERR_UNSUPPORTED;  // rows of Q and O are 32-bit numbers
     if ((int64_t)page_size * max_blocks > ((int64_t)1 << 30) || (int64_t)num_pages * page_size >= ((int64_t)1 << 31))
         return GQE_ERR_UNSUPPORTED;
     st = check_workspace(workspace, workspace_bytes, kStatusBytes + chunk_scratch_bytes(s));

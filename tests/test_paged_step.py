@@ -79,6 +79,8 @@ def test_attention_refuses_shapes(g):
     assert call(1, 8, 64, 8, 2, 96, 2, g.GQE_BF16) == 2
     assert call(1, 8, 64, 8, 3, 128, 2, g.GQE_BF16) == 1
     assert call(1, 8, 64, 64, 2, 128, 17, g.GQE_BF16) == 2
+    assert call(1, 1 << 23, 64, 256, 2, 32, 2, g.GQE_BF16) == 2  # T * h of 2^31
+    assert call(1, 1 << 23, 64, 256, 2, 32, 2, g.GQE_F32) == 2
     assert g.gqe_chunk_workspace_bytes(g.make_shape(1, 8, 64, 8, 3, 128, 2, g.GQE_BF16)) == 0
 
 
