@@ -97,7 +97,7 @@ struct Smem {
     uint64_t item_full[kItems], rows_full[kItems], item_free[kItems];
     uint64_t kv_full_k[kStages], kv_full_v[kStages], kv_empty_k[kStages], kv_empty_v[kStages];
     uint64_t s_full[kQT], p_empty[kQT], o_full[kQT], q_full[kQT], q_empty[kQT], p_full[kQT], o_empty[kQT], st_free[kQT], vote[kQT], qm_full[kQT];
-    uint64_t x_full, x_free, s_free, mma_drain, mma_drain2;
+    uint64_t x_full, x_free, s_free, mma_drain, mma_drain2, kind_done;
     uint32_t tmem_base;
     int32_t abort_flag;
 };
@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t bar_count(int i) {
     return i < kFree ? 1 : i < kLoads ? (kGather ? 14 : 11) : i < kOnes ? (kGather ? 128 : 1) : i < kWarps ? 1 : i < kTail ? 4 : 1;
 }
 template <int kH>
-constexpr int bar_total() { return 3 * kItems + 4 * Smem<kH>::kStages + 10 * kQT + 5; }
+constexpr int bar_total() { return 3 * kItems + 4 * Smem<kH>::kStages + 10 * kQT + 6; }
 
 struct Params {
     const bf16* Q;
@@ -391,7 +391,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
     }
     if (steps > 1) {  // both groups took part: group 1 hands its state to group 0
         if (t == 1) {
-            if (!warp_wait(sm, &sm.x_free, (swaps & 1) ^ 1, 50)) return false;
+            if (!warp_wait(sm, &sm.x_free, swaps & 1, 50)) return false;
             ++swaps;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -606,6 +606,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 if (!sm.has[slot]) {
                     mbar_arrive(&sm.item_free[slot]);
                     if (++ends == phases) break;
+                    // The first kind's S have read their Q: the buffers may change hands.
+                    // A barrier of its own, as who waits here has not followed q_empty's
+                    // phases (or has no such barrier: the tiles of many rows).
+                    umma_commit(&sm.kind_done);
                     few = !few;
                     continue;
                 }
@@ -656,8 +660,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     umma_commit(&sm.kv_empty_k[st]);
                 }
                 if (!ok) break;
-                if (qb == 0) umma_commit(&sm.q_empty[0]);
-                if (few ? qb == 1 : tiles == 2) umma_commit(&sm.q_empty[1]);
+                if (few) umma_commit(&sm.q_empty[qb]);
             }
             umma_commit(&sm.mma_drain);  // all issued MMAs complete before TMEM is released
             bar_wait(&sm.mma_drain, 0);
@@ -675,7 +678,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             tok[e] = r < u.W * u.k ? token : INT_MIN / 2;
             sel[e] = r - token * u.k;
         }
-        uint32_t ui = 0, few_it = 0, q_fill[kQT] = {0, 0};
+        uint32_t ui = 0, few_it = 0;
         bool ok = true;
 #pragma unroll 1
         for (int phase = 0; phase < phases && ok; ++phase) {
@@ -696,7 +699,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     ++ui;
                     break;
                 }
-                const int tiles = it.nt > u.W ? 2 : 1;
                 int row[kQT][4];  // the lane's rows of Q
 #pragma unroll
                 for (int t = 0; t < kQT; ++t)
@@ -705,14 +707,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         const int off = tok[e] + t * u.W;
                         row[t][e] = off >= 0 && off < it.nt ? u.idx[((int64_t)(it.t0 + off) * u.g + it.q) * u.k + sel[e]] : -1;
                     }
-                auto publish = [&]() {
-                    if (lane == 0) {
-                        sm.has[slot] = 1;
-                        sm.item[slot] = it;
-                        mbar_arrive(&sm.item_full[slot]);
-                    }
-                    __syncwarp();
-                };
                 if (lane == 0) {
                     sm.has[slot] = 1;
                     sm.item[slot] = it;
@@ -729,14 +723,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         sm.row[slot][t][lane * 4 + e] = good ? (it.t0 + off) * u.h + j : -1;
                     }
                 warp_arrive(&sm.rows_full[slot]);
-                if (!few) {  // the softmax warps copy the tiles
-                    ++q_fill[0];
-                    if (tiles == 2) ++q_fill[1];
-                    continue;
-                }
-                const int buf = few_it++ & 1;
-                if (!warp_wait(sm, &sm.q_empty[buf], ((buf ? q_fill[1] : q_fill[0]) & 1) ^ 1, 21)) { ok = false; break; }
-                if (buf) ++q_fill[1]; else ++q_fill[0];
+                if (!few) continue;  // the softmax warps copy the tiles
+                const int buf = few_it & 1;
+                if (phase && !warp_wait(sm, &sm.kind_done, 0, 22)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.q_empty[buf], ((few_it >> 1) & 1) ^ 1, 21)) { ok = false; break; }
+                ++few_it;
                 copy_rows<kH, 4>(smem_u32(sm.q[buf]), p.Q, d, sm.row[slot][0], kFew, d);
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();  // from the generic to the tensor cores' view
@@ -834,7 +825,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const int sel = r - (r * u.inv_k >> 16) * u.k;
         const bool in_tile = r < u.W * u.k;
         const uint64_t C2 = pk2(p.scale_log2, p.scale_log2);
-        uint32_t ctile = 0, o_it = 0, votes = 0, swaps = 0, few_items = 0;
+        uint32_t ctile = 0, o_it = 0, votes = 0, swaps = 0;
         uint32_t ui = 0;
         // The next item of the kind, or null at its end (or after a failure).
         auto take = [&]() -> const ChunkItem* {
@@ -876,11 +867,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
 #pragma unroll 1
         for (int phase = 0; phase < phases; ++phase) {
         if ((phase == 0) == few_first) {
+            // x is free for group 1's first hand-over once group 0 has no stage in it
+            if (t == 0) warp_arrive(&sm.x_free);
             while (const ChunkItem* next = take()) {
                 const ChunkItem it = *next;
                 const int slot = ui % kItems;
                 if (!warp_wait(sm, &sm.rows_full[slot], (ui / kItems) & 1, 41)) break;
-                ++few_items;
                 if (t == 0) zero_fill(it, it.nt);
                 if (!(it.nt * u.k <= 4 ? few_item<4, kH>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)
                                        : few_item<16, kH>(u, p, sm, it, slot, t, tmem, ctile, o_it, votes, swaps)))
@@ -888,11 +880,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 done();
             }
             if (phase + 1 == phases) continue;
-            // The last few-row items' products have read the Q buffer that the many
-            // rows' tile t takes, and group 0 has read what group 1 handed over: x is
-            // the stages' now.
-            if (few_items > t && !aborted(sm)) warp_wait(sm, &sm.q_empty[t], ((few_items - t + 1) / 2 - 1) & 1, 53);
-            if (swaps > 0 && !aborted(sm)) warp_wait(sm, &sm.x_free, (swaps - 1) & 1, 52);
+            // The few-row items' products have read the Q buffers, and group 0 has read
+            // what group 1 handed over: the tiles' and the stages' now.
+            if (!aborted(sm)) warp_wait(sm, &sm.kind_done, 0, 53);
+            if (!aborted(sm)) warp_wait(sm, &sm.x_free, swaps & 1, 52);
             continue;
         }
         // This warp's rows of an item's Q tile, in flight until q_ready.
@@ -1229,7 +1220,6 @@ cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a, const CUtensorM
 cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
     const gqe_shape& s = *a.s;
     const int page = 1 << a.page_shift;
-    if ((int64_t)s.T * s.h >= ((int64_t)1 << 31) - 1) return cudaErrorNotSupported;
     // Pages of 16 rows or more by the TMA, a box per page and 64-element part; of
     // fewer rows by copies, row by row: at 8 rows a page the boxes' number held 64
     // decodes at 3.8 TB/s (16 rows: 5.8), at 4 rows the TMA's gather of four rows at a

@@ -224,6 +224,29 @@ STEPS = {
     "bf16 d64": dict(new=[65, 1, 300], ctx=[10, 700, 64], d=64, k=3, h=12),
     "bf16 d64 window": dict(new=[65, 1, 300], ctx=[10, 700, 64], d=64, window=70, sinks=4),
     "bf16 d32": dict(new=[33, 1], ctx=[100, 500], d=32, k=4, ps=4),
+    # more requests than a block has threads: each thread of the split sums several
+    "many requests": dict(new=[1] * 700 + [20] + [0, 3, 1] * 100, ctx=[(29 * i) % 97 for i in range(1001)], h=4, gr=2, k=1, pad=2),
+    "many chunks": dict(new=[(i * 7) % 41 for i in range(530)], ctx=[(13 * i) % 150 for i in range(530)], h=4, gr=2, k=2, ps=32),
+    # every block goes from one kind of unit to the other, in either order
+    "many chunks k1 ps4": dict(new=[(i * 7) % 41 for i in range(530)], ctx=[(13 * i) % 150 for i in range(530)], h=8, gr=2, k=1, ps=4),
+    "many chunks d64": dict(new=[(i * 7) % 41 for i in range(300)], ctx=[(113 * i) % 450 for i in range(300)], h=4, gr=2, k=2, d=64),
+    "many chunks long": dict(new=[(i * 17) % 91 if i % 3 else 1 for i in range(300)], ctx=[(113 * i) % 450 for i in range(300)], h=16, gr=4, k=4, ps=64),
+    "f32 many requests": dict(new=[1, 2, 1, 9] * 200, ctx=[(31 * i) % 90 for i in range(800)], h=4, gr=2, k=1, d=32, dtype=F32),
+    # several items of both kinds for every block, some of them split
+    "many items": dict(new=[1] * 300 + [70, 3, 200], ctx=[500 + (17 * i) % 300 for i in range(303)], h=16, gr=4, k=2, ps=32),
+    "many items ps4": dict(new=[1] * 200 + [150, 3, 300], ctx=[300 + (17 * i) % 300 for i in range(203)], h=16, gr=4, k=2, ps=4),
+    "many items f32": dict(new=[1] * 150 + [33, 5, 150], ctx=[300 + (17 * i) % 300 for i in range(153)], h=8, gr=4, k=1, d=64, dtype=F32),
+    # copied pages (fewer than 16 rows), every head width, 5 .. 16 and 17 .. 128 query rows beside decodes and prompts
+    **{f"rows d{d} ps{ps}": dict(new=[1, 90, 3, 1, 257, 8, 9, 64, 65], ctx=[400, 0, 64, 1, 700, 290, 130, 5, 127], d=d, ps=ps)
+       for d, ps in ((128, 1), (128, 8), (64, 1), (64, 8), (32, 2), (32, 16))},
+    **{f"rows window d{d} ps{ps}": dict(new=[1, 90, 3, 1, 257, 8], ctx=[400, 0, 364, 1, 700, 290], d=d, ps=ps, window=140,
+                                        sinks=9, k=3, h=14) for d, ps in ((128, 2), (64, 4), (32, 1))},
+    "f32 few rows": dict(new=[1, 2, 3, 4, 5, 16, 17], ctx=[200, 65, 190, 63, 0, 9, 300], k=1, dtype=F32, ps=8),
+    "f32 few rows window": dict(new=[1, 2, 3, 4, 1], ctx=[200, 65, 190, 63, 700], k=1, dtype=F32, d=64, ps=1, window=40, sinks=70),
+    "f32 k4": dict(new=[1, 1, 1], ctx=[129, 64, 63], h=8, gr=2, k=4, d=32, dtype=F32),
+    "heads of 256": dict(new=[1, 20], ctx=[90, 200], h=256, gr=1, k=16, d=64),
+    "f32 heads of 256": dict(new=[1, 20], ctx=[90, 200], h=256, gr=2, k=3, d=32, dtype=F32),
+    "page of 4096": dict(new=[1, 100], ctx=[5000, 100], ps=4096),
     "peaked": dict(new=[40, 1], ctx=[400, 300], scale=4.0),
 }
 
@@ -292,6 +315,66 @@ def test_later_tokens_do_not_reach_earlier_rows(kw, which):
     n = st.cu[-1]
     ok = ~hit[:n] if which != "K" else ~hit[:n]
     assert ((st.O[:n].double() - O[:n]).abs() <= tol[:n])[ok].all()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(ps=4, d=64), dict(dtype=F32, d=64)], ids=["bf16", "bf16 ps4", "f32"])
+def test_one_request_of_nan(kw):
+    """A request whose values are all NaN, split over many blocks, leaves the others as they are."""
+    st = Step(U.gqe(), new=[1, 300, 1, 1], ctx=[90, 900, 9000, 64], gr=2, seed=12, **kw)
+    for b in (1, 2):
+        st.V.view(-1, *st.V.shape[2:])[st.rows_of(b)] = float("nan")
+    st.run()
+    assert st.status() == 0
+    O, mag, wob = R.attention(st.Q, st.K, torch.nan_to_num(st.V), st.table, st.cu, st.lengths, 0, 0, st.idx, st.gate)
+    tol = R.tolerance(O, mag, wob, st.dtype, max(st.lengths))
+    chosen = torch.zeros(O.shape[:2], dtype=torch.bool, device="cuda")
+    chosen[torch.arange(O.shape[0], device="cuda")[:, None], st.idx.flatten(1).long()] = True
+    for b in (0, 3):
+        rows = slice(st.cu[b], st.cu[b + 1])
+        assert ((st.O[rows].double() - O[rows]).abs() <= tol[rows]).all()
+    for b in (1, 2):
+        rows = slice(st.cu[b], st.cu[b + 1])
+        assert torch.isnan(st.O[rows][chosen[rows]]).all() and (st.O[rows][~chosen[rows]] == 0).all()
+
+
+@pytest.mark.parametrize("kw", [dict(ps=64), dict(ps=8), dict(ps=64, dtype=F32)], ids=["pages", "copied pages", "f32"])
+def test_cache_offsets_past_32_bits(kw):
+    """Pages whose first element is behind 2^31 elements (bf16 rows of 2 KB behind 4 GB; fp32 behind 8 GB)."""
+    g = U.gqe()
+    st = Step(g, new=[1, 70, 1], ctx=[300, 10, 999], h=16, gr=8, k=1, seed=13, **kw)
+    first = (1 << 31) // (st.ps * 8 * 128) + 1
+    pages = first + st.num_pages
+    big = [torch.empty(pages, *x.shape[1:], dtype=x.dtype, device="cuda") for x in (st.K, st.V)]
+    # the requests' rows go in by the append
+    rows = sum(st.lengths)
+    flat = torch.cat([st.rows_of(b) for b in range(3)])
+    slots = (flat + first * st.ps).to(torch.int32)
+    src = [x.view(-1, 8, 128)[flat].contiguous() for x in (st.K, st.V)]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    g.gqe_kv_append(g.make_shape(1, rows, 64, 8, 8, 128, 1, st.dtype), *src, slots, *big, ws)
+    assert g.gqe_get_device_status(ws) == 0
+    small = st.K, st.V
+    st.K, st.V = big
+    st.bt = torch.where(st.bt >= 0, st.bt + first, st.bt)
+    st.run()
+    assert st.status() == 0
+    st.K, st.V = small
+    st.check()
+
+
+def test_two_calls_at_once():
+    """Two steps on two streams, each with its own workspace."""
+    g = U.gqe()
+    steps = [Step(g, new=[1] * 40 + [100 * i], ctx=[30 * j for j in range(41)], seed=i, window=i and 200, sinks=4) for i in (0, 1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for st, s in zip(steps, streams):
+            st.run(s)
+    torch.cuda.synchronize()
+    for st in steps:
+        assert st.status() == 0
+        st.check()
 
 
 def test_bad_requests_are_reported_and_skipped():
