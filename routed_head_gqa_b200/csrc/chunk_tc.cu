@@ -74,11 +74,15 @@ template <int kH>
 struct Smem {
     static constexpr uint32_t kTile = kH * kHalf;  // bytes of a Q, K or V tile
     static constexpr int kStages = 4 / kH;         // K and V tiles in flight, each
-    uint8_t q[kQT][kTile];
-    uint8_t k[kStages][kTile];
-    uint8_t v[kStages][kTile];
+    // Q_0, the K stages, the V stages, Q_1.  Few rows, whose Q is small, have Q_0 and
+    // Q_1 as one more stage.
+    uint8_t tile[2 * kStages + 2][kTile];
+    uint8_t qf[2][kH * kFew * 128];      // few rows: Q, for two items
     uint8_t p[kQT][kFew * 256];          // few rows: P_t [16 rows][128 keys] bf16, two 64-key halves
     float x[kFew][128];                  // few rows: O^T_1 on its way to warpgroup 0
+    __device__ __forceinline__ uint8_t* q(int t) { return tile[t ? 2 * kStages + 1 : 0]; }
+    __device__ __forceinline__ uint8_t* k(bool few, int st) { return tile[st + (few ? 0 : 1)]; }
+    __device__ __forceinline__ uint8_t* v(int st) { return tile[kStages + 1 + st]; }
     // Many rows: 64 bytes of each of a softmax warp's 32 rows on their way out, in a
     // half of the group's own p and of x.
     __device__ __forceinline__ uint4* stage(int t, int w) {
@@ -95,9 +99,10 @@ struct Smem {
     ChunkSplit split;
     // barriers, in the order of kBarCounts
     uint64_t item_full[kItems], rows_full[kItems], item_free[kItems];
-    uint64_t kv_full_k[kStages], kv_full_v[kStages], kv_empty_k[kStages], kv_empty_v[kStages];
+    // by kind: the many rows' kStages stages, the few's one more
+    uint64_t kv_full_k[2 * kStages + 1], kv_full_v[2 * kStages + 1], kv_empty_k[2 * kStages + 1], kv_empty_v[2 * kStages + 1];
     uint64_t s_full[kQT], p_empty[kQT], o_full[kQT], q_full[kQT], q_empty[kQT], p_full[kQT], o_empty[kQT], st_free[kQT], vote[kQT], qm_full[kQT];
-    uint64_t x_full, x_free, s_free, mma_drain, mma_drain2, kind_done;
+    uint64_t x_full, x_free, s_free, mma_drain, mma_drain2, kind_done, kind_done_v;
     uint32_t tmem_base;
     int32_t abort_flag;
 };
@@ -107,12 +112,41 @@ struct Smem {
 // the 128 threads of those, the four warps of a warpgroup, or one.
 template <int kH, bool kGather>
 __device__ __forceinline__ uint32_t bar_count(int i) {
-    constexpr int kS = Smem<kH>::kStages, kFree = 2 * kItems, kLoads = 3 * kItems, kOnes = kLoads + 2 * kS,
+    constexpr int kS = 2 * Smem<kH>::kStages + 1, kFree = 2 * kItems, kLoads = 3 * kItems, kOnes = kLoads + 2 * kS,
                   kWarps = kOnes + 2 * kS + 5 * kQT, kTail = kWarps + 5 * kQT + 3;
     return i < kFree ? 1 : i < kLoads ? (kGather ? 14 : 11) : i < kOnes ? (kGather ? 128 : 1) : i < kWarps ? 1 : i < kTail ? 4 : 1;
 }
 template <int kH>
-constexpr int bar_total() { return 3 * kItems + 4 * Smem<kH>::kStages + 10 * kQT + 6; }
+constexpr int bar_total() { return 3 * kItems + 8 * Smem<kH>::kStages + 4 + 10 * kQT + 7; }
+
+// Place in the ring of K/V stages, and the parity of its round.  The two kinds of
+// units have rings of their own, kStages or one more, with barriers of their own.
+template <int kStages>
+struct Ring {
+    int st;
+    uint32_t phase;
+    bool few;
+    __device__ __forceinline__ explicit Ring(bool few) : st(0), phase(0), few(few) {}
+    __device__ __forceinline__ int bar() const { return few ? kStages + st : st; }
+    __device__ __forceinline__ int size() const { return kStages + (few ? 1 : 0); }
+    __device__ __forceinline__ void next() {
+        if (++st == size()) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void prev() {
+        if (--st < 0) {
+            st = size() - 1;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void turn() {  // to the other kind
+        st = 0;
+        phase = 0;
+        few = !few;
+    }
+};
 
 struct Params {
     const bf16* Q;
@@ -232,7 +266,8 @@ __device__ __forceinline__ void issue_st(uint32_t tmem, uint32_t dhi, int t, uin
 #pragma unroll
     for (int kk = 0; kk < 4 * kH; ++kk) {
         const uint32_t off = (uint32_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-        umma_ss(tmem + kColS + 64 * t, smem_desc_join(k_lo + off, dhi), smem_desc_join(q_lo + off, dhi), idesc, kk > 0 ? 1u : 0u);
+        const uint32_t q_off = (uint32_t)(((kk >> 2) * kFew * 128 + (kk & 3) * 32) >> 4);
+        umma_ss(tmem + kColS + 64 * t, smem_desc_join(k_lo + off, dhi), smem_desc_join(q_lo + q_off, dhi), idesc, kk > 0 ? 1u : 0u);
     }
 }
 __device__ __forceinline__ void issue_pvt(uint32_t tmem, uint32_t dhi, int t, uint32_t v_lo, uint32_t p_lo, bool first) {
@@ -441,12 +476,12 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
 
 // Copies rows of 64 kH elements (of which d exist, the others zeros) to a 128-byte
 // swizzled tile, 16 bytes a lane, whole rows of adjacent lanes.  at: the rows'
-// indexes in shared memory, -1 for a row of zeros.
+// indexes in shared memory, -1 for a row of zeros; half: bytes between its 64-element parts.
 template <int kH, int kUnroll>
-__device__ __forceinline__ void copy_rows(uint32_t tile, const bf16* base, int64_t stride, const int32_t* at, int rows, int d) {
+__device__ __forceinline__ void copy_rows(uint32_t tile, uint32_t half, const bf16* base, int64_t stride, const int32_t* at, int rows, int d) {
     constexpr int kPer = 4 / kH;  // rows a copy
     const int lane = threadIdx.x & 31, sub = lane / (8 * kH), c = lane % (8 * kH);
-    const uint32_t dst = tile + (c >> 3) * kHalf + sub * 128;
+    const uint32_t dst = tile + (c >> 3) * half + sub * 128;
     const bool in = kH == 2 || c * 8 < d;
     const bf16* src = base + c * 8;
 #pragma unroll kUnroll
@@ -473,8 +508,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     const int d = kH == 2 ? 128 : p.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    static_assert(kBars <= 64, "one barrier per thread of warps 1 and 2");
-    if (warp == 1 || warp == 2) {
+    static_assert(kBars <= 96, "one barrier per thread of warps 1 to 3");
+    if (warp >= 1 && warp <= 3) {
         if (tid - 32 < kBars) mbar_init(&sm.item_full[0] + (tid - 32), bar_count<kH, kGather>(tid - 32));
         fence_barrier_init();
     }
@@ -519,8 +554,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const int shift = u.page_shift;
         const int box_rows = shift >= 7 ? kBN : 1 << shift;
         const int boxes = kBN / box_rows;  // per tile and 64-element part
-        uint32_t kv_it = 0;
-        bool k_pending = false;
+        Ring<kStages> ring(few_first);
+        int issued = 0;       // steps of this kind
+        bool k_pending = false, turned = false;
         bool ok = true;
         if (!kGather && lane == 0) {
             tma_prefetch_desc(&mapK);
@@ -533,13 +569,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             if (!sm.has[slot]) {
                 warp_arrive(&sm.item_free[slot]);
                 if (++ends == phases) break;
+                ring.turn();
+                issued = 0;
+                turned = true;
                 continue;
             }
             const ChunkItem it = sm.item[slot];
 #pragma unroll 1
-            for (int s = it.s0; s < it.s1; ++s, ++kv_it) {
-                const int st = kv_it % kStages, x0 = s * kBN;
-                const uint32_t par = ((kv_it / kStages) & 1) ^ 1;
+            for (int s = it.s0; s < it.s1; ++s, ++issued, ring.next()) {
+                const int b = ring.bar(), x0 = s * kBN;
+                const uint32_t par = ring.phase ^ 1;
                 int page = 0, in_page = 0;
                 if constexpr (kGather) {
                     const int key = it.key(x0 + quarter * 32 + lane);
@@ -556,7 +595,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 }
                 auto load = [&](const CUtensorMap* map, const bf16* pages, uint64_t* bar, uint8_t* dst) {
                     if constexpr (kGather) {
-                        copy_rows<kH, 4>(smem_u32(dst) + quarter * 32 * 128, pages + (int64_t)it.q * d, (int64_t)u.g * d,
+                        copy_rows<kH, 4>(smem_u32(dst) + quarter * 32 * 128, kHalf, pages + (int64_t)it.q * d, (int64_t)u.g * d,
                                          sm.kv_row[quarter], kBN / 4, d);
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
                     } else {
@@ -568,31 +607,35 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         }
                     }
                 };
-                if (!warp_wait(sm, &sm.kv_empty_k[st], par, 2)) { ok = false; break; }
-                load(&mapK, p.K, &sm.kv_full_k[st], sm.k[st]);
+                // the second kind's stages lie in the first's memory
+                if (turned && !warp_wait(sm, &sm.kind_done, 0, 4)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.kv_empty_k[b], par, 2)) { ok = false; break; }
+                load(&mapK, p.K, &sm.kv_full_k[b], sm.k(ring.few, ring.st));
                 k_pending = true;
-                if (!warp_wait(sm, &sm.kv_empty_v[st], par, 3)) { ok = false; break; }
-                load(&mapV, p.V, &sm.kv_full_v[st], sm.v[st]);
+                if (turned && !warp_wait(sm, &sm.kind_done_v, 0, 5)) { ok = false; break; }
+                if (!warp_wait(sm, &sm.kv_empty_v[b], par, 3)) { ok = false; break; }
+                load(&mapV, p.V, &sm.kv_full_v[b], sm.v(ring.st));
                 k_pending = false;
             }
             warp_arrive(&sm.item_free[slot]);
         }
         // Drain: every issued load lands before the CTA may exit.
-        if (k_pending) bar_wait(&sm.kv_full_k[kv_it % kStages], (kv_it / kStages) & 1);
+        if (k_pending) bar_wait(&sm.kv_full_k[ring.bar()], ring.phase);
 #pragma unroll 1
-        for (uint32_t back = 1; back <= kStages && back <= kv_it; ++back) {
-            const uint32_t i = kv_it - back;
-            bar_wait(&sm.kv_full_k[i % kStages], (i / kStages) & 1);
-            bar_wait(&sm.kv_full_v[i % kStages], (i / kStages) & 1);
+        for (int back = min(issued, ring.size()); back > 0; --back) {
+            ring.prev();
+            bar_wait(&sm.kv_full_k[ring.bar()], ring.phase);
+            bar_wait(&sm.kv_full_v[ring.bar()], ring.phase);
         }
     } else if (warp == 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: S
         if (lane == 0) {
             const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
-            const uint32_t q_lo0 = smem_desc_lo(smem_u32(sm.q[0]), 16), q_lo1 = smem_desc_lo(smem_u32(sm.q[1]), 16);
-            const uint32_t k_lo0 = smem_desc_lo(smem_u32(sm.k[0]), 16);
-            uint32_t kv_it = 0, s_cnt = 0, st_cnt[kQT] = {0, 0};
+            const uint32_t q_lo0 = smem_desc_lo(smem_u32(sm.q(0)), 16), q_lo1 = smem_desc_lo(smem_u32(sm.q(1)), 16);
+            const uint32_t qf_lo = smem_desc_lo(smem_u32(sm.qf[0]), 16);
+            Ring<kStages> ring(few_first);
+            uint32_t s_cnt = 0, st_cnt[kQT] = {0, 0};
             bool ok = true;
             // the S buffer is free: its last reader of either form is done
             auto s_buffer = [&]() { return s_cnt == 0 || bar_wait(&sm.s_free, (s_cnt - 1) & 1); };
@@ -606,11 +649,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 if (!sm.has[slot]) {
                     mbar_arrive(&sm.item_free[slot]);
                     if (++ends == phases) break;
-                    // The first kind's S have read their Q: the buffers may change hands.
-                    // A barrier of its own, as who waits here has not followed q_empty's
-                    // phases (or has no such barrier: the tiles of many rows).
-                    umma_commit(&sm.kind_done);
+                    umma_commit(&sm.kind_done);  // the first kind's S have read their Q and K
                     few = !few;
+                    ring.turn();
                     continue;
                 }
                 const int n = sm.item[slot].s1 - sm.item[slot].s0;
@@ -620,7 +661,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 // Q: few rows, the buffers in turn, filled by warp 2; many, one per tile,
                 // filled by the tile's softmax warps
                 const int qb = few ? few_it++ & 1 : 0;
-                const uint32_t q_lo = qb ? q_lo1 : q_lo0;
+                const uint32_t q_lo = qf_lo + qb * (sizeof(sm.qf[0]) >> 4);
                 for (int t = 0; t < kQT && ok; ++t) {
                     if (few ? t != qb : t > 0 && tiles < 2) continue;
                     if (few) {
@@ -634,10 +675,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 if (!ok) { fail(sm, 11); break; }
                 if (few ? !s_buffer() : !(st_buffer(0) && st_buffer(1))) { fail(sm, 14); break; }
 #pragma unroll 1
-                for (int i = 0; i < n && ok; ++i, ++kv_it) {
-                    const int st = kv_it % kStages;
-                    const uint32_t k_lo = k_lo0 + st * (kTileBytes >> 4);
-                    if (!bar_wait(&sm.kv_full_k[st], (kv_it / kStages) & 1)) { fail(sm, 12); ok = false; break; }
+                for (int i = 0; i < n && ok; ++i, ring.next()) {
+                    const uint32_t k_lo = smem_desc_lo(smem_u32(sm.k(few, ring.st)), 16);
+                    if (!bar_wait(&sm.kv_full_k[ring.bar()], ring.phase)) { fail(sm, 12); ok = false; break; }
                     if (kGather) fence_proxy_async_smem();  // rows written by plain copies
                     if (few) {
                         const int t = i & 1;
@@ -657,7 +697,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         ++s_cnt;
                     }
                     if (!ok) break;
-                    umma_commit(&sm.kv_empty_k[st]);
+                    umma_commit(&sm.kv_empty_k[ring.bar()]);
                 }
                 if (!ok) break;
                 if (few) umma_commit(&sm.q_empty[qb]);
@@ -725,10 +765,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 warp_arrive(&sm.rows_full[slot]);
                 if (!few) continue;  // the softmax warps copy the tiles
                 const int buf = few_it & 1;
-                if (phase && !warp_wait(sm, &sm.kind_done, 0, 22)) { ok = false; break; }
                 if (!warp_wait(sm, &sm.q_empty[buf], ((few_it >> 1) & 1) ^ 1, 21)) { ok = false; break; }
                 ++few_it;
-                copy_rows<kH, 4>(smem_u32(sm.q[buf]), p.Q, d, sm.row[slot][0], kFew, d);
+                copy_rows<kH, 4>(smem_u32(sm.qf[buf]), kFew * 128, p.Q, d, sm.row[slot][0], kFew, d);
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();  // from the generic to the tensor cores' view
                 warp_arrive(&sm.q_full[buf]);
@@ -738,10 +777,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: O += P V
         const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
-        const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v[0]), kH == 2 ? kHalf : 0);
+        const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v(0)), kH == 2 ? kHalf : 0);
         const uint32_t p_lo0 = smem_desc_lo(smem_u32(sm.p[0]), 16), p_lo1 = smem_desc_lo(smem_u32(sm.p[1]), 16);
         const int page = 1 << u.page_shift;
-        uint32_t kv_it = 0, c[kQT] = {0, 0}, o_cnt[kQT] = {0, 0};
+        Ring<kStages> ring(few_first);
+        uint32_t c[kQT] = {0, 0}, o_cnt[kQT] = {0, 0};
         bool ok = true;
         bool few = few_first;
 #pragma unroll 1
@@ -751,22 +791,25 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
             if (!sm.has[slot]) {
                 warp_arrive(&sm.item_free[slot]);
                 if (++ends == phases) break;
+                if (lane == 0) umma_commit(&sm.kind_done_v);  // its O have read their V
+                __syncwarp();
                 few = !few;
+                ring.turn();
                 continue;
             }
             const ChunkItem it = sm.item[slot];
             warp_arrive(&sm.item_free[slot]);
             const int n = it.s1 - it.s0, n0 = tile_steps(u, it, 0, few), n1 = tile_steps(u, it, 1, few);
 #pragma unroll 1
-            for (int i = 0; i < n && ok; ++i, ++kv_it) {
-                const int st = kv_it % kStages;
-                if (!warp_wait(sm, &sm.kv_full_v[st], (kv_it / kStages) & 1, 31)) { ok = false; break; }
+            for (int i = 0; i < n && ok; ++i, ring.next()) {
+                const int st = ring.st;
+                if (!warp_wait(sm, &sm.kv_full_v[ring.bar()], ring.phase, 31)) { ok = false; break; }
                 if (kGather) fence_proxy_async_smem();
                 // Rows of loaded pages that no row of the unit sees: past the last
                 // token, and between the first `sinks` keys and the window.
                 const int x0 = (it.s0 + i) * kBN, x1 = x0 + kBN;  // of the key list
                 if (x1 > it.hi - it.skip || (u.window && x0 < it.lo - it.skip)) {
-                    uint8_t* v = sm.v[st];
+                    uint8_t* v = sm.v(st);
                     auto zero = [&](int a, int b) {
                         a = max(a, x0);
                         b = min(b, x1);
@@ -803,7 +846,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     if (j == 0) ++o_cnt[t];
                 }
                 if (!ok) break;
-                if (lane == 0) umma_commit(&sm.kv_empty_v[st]);
+                if (lane == 0) umma_commit(&sm.kv_empty_v[ring.bar()]);
                 __syncwarp();
             }
         }
@@ -880,15 +923,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 done();
             }
             if (phase + 1 == phases) continue;
-            // The few-row items' products have read the Q buffers, and group 0 has read
-            // what group 1 handed over: the tiles' and the stages' now.
-            if (!aborted(sm)) warp_wait(sm, &sm.kind_done, 0, 53);
+            // The few-row items' products have read the stage that lies in the Q tiles, and
+            // group 0 has read what group 1 handed over, where the epilogue's stages lie.
+            if (!aborted(sm)) warp_wait(sm, t ? &sm.kind_done_v : &sm.kind_done, 0, 53);
             if (!aborted(sm)) warp_wait(sm, &sm.x_free, swaps & 1, 52);
             continue;
         }
         // This warp's rows of an item's Q tile, in flight until q_ready.
         auto load_q = [&](int slot) {
-            copy_rows<kH, 4>(smem_u32(sm.q[t]) + wq * 32 * 128, p.Q, d, sm.row[slot][t] + wq * 32, 32, d);
+            copy_rows<kH, 4>(smem_u32(sm.q(t)) + wq * 32 * 128, kHalf, p.Q, d, sm.row[slot][t] + wq * 32, 32, d);
         };
         auto q_ready = [&]() {
             asm volatile("cp.async.wait_all;" ::: "memory");
