@@ -53,7 +53,7 @@ using bf16 = __nv_bfloat16;
 constexpr int kBM = 128, kBN = 128, kQT = 2;
 constexpr int kFew = 16;                   // query rows up to which a unit is turned around
 constexpr int kItems = 4;                  // items in flight between the walk and the other roles
-constexpr uint32_t kHalf = 128 * 64 * 2;   // 64 elements of 128 rows, 16 KB
+constexpr uint32_t kPart = 8 * 64 * 2;     // 64 elements of 8 rows, a swizzle atom
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: p <= 2^8 between rescales
@@ -72,7 +72,10 @@ struct Split {
 // padded with zeros).
 template <int kH>
 struct Smem {
-    static constexpr uint32_t kTile = kH * kHalf;  // bytes of a Q, K or V tile
+    // A Q, K or V tile: groups of 8 rows, the kH parts of a group one after the other,
+    // so that one box fetches both parts of a page (a box per page and part held 16-row
+    // pages at 5.8 TB/s).
+    static constexpr uint32_t kTile = kBM / 8 * kH * kPart;
     static constexpr int kStages = 4 / kH;         // K and V tiles in flight, each
     // Q_0, the K stages, the V stages, Q_1.  Few rows, whose Q is small, have Q_0 and
     // Q_1 as one more stage.
@@ -243,7 +246,7 @@ __device__ __forceinline__ void issue_s(uint32_t tmem, uint32_t dhi, uint32_t q_
     constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, false, false);
 #pragma unroll
     for (int kk = 0; kk < 4 * kH; ++kk) {
-        const uint32_t off = (uint32_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+        const uint32_t off = (uint32_t)(((kk >> 2) * kPart + (kk & 3) * 32) >> 4);
         umma_ss(tmem + kColS, smem_desc_join(q_lo + off, dhi), smem_desc_join(k_lo + off, dhi), idesc, kk > 0 ? 1u : 0u);
     }
 }
@@ -253,7 +256,7 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t dhi, int t, uin
     constexpr uint32_t idesc = idesc_bf16_f32(kBM, 64 * kH, false, true);
 #pragma unroll
     for (int kk = 0; kk < kBN / 16; ++kk)
-        umma_ts(tmem + kColO + t * 128, tmem + kColP + 64 * t + kk * 8, smem_desc_join(v_lo + (uint32_t)((kk * 2048) >> 4), dhi),
+        umma_ts(tmem + kColO + t * 128, tmem + kColP + 64 * t + kk * 8, smem_desc_join(v_lo + (uint32_t)((kk * 2 * kH * kPart) >> 4), dhi),
                 idesc, first && kk == 0 ? 0u : 1u);
 }
 
@@ -265,17 +268,17 @@ __device__ __forceinline__ void issue_st(uint32_t tmem, uint32_t dhi, int t, uin
     constexpr uint32_t idesc = idesc_bf16_f32(kBN, kFew, false, false);
 #pragma unroll
     for (int kk = 0; kk < 4 * kH; ++kk) {
-        const uint32_t off = (uint32_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-        const uint32_t q_off = (uint32_t)(((kk >> 2) * kFew * 128 + (kk & 3) * 32) >> 4);
-        umma_ss(tmem + kColS + 64 * t, smem_desc_join(k_lo + off, dhi), smem_desc_join(q_lo + q_off, dhi), idesc, kk > 0 ? 1u : 0u);
+        const uint32_t off = (uint32_t)(((kk >> 2) * kPart + (kk & 3) * 32) >> 4);
+        umma_ss(tmem + kColS + 64 * t, smem_desc_join(k_lo + off, dhi), smem_desc_join(q_lo + off, dhi), idesc, kk > 0 ? 1u : 0u);
     }
 }
-__device__ __forceinline__ void issue_pvt(uint32_t tmem, uint32_t dhi, int t, uint32_t v_lo, uint32_t p_lo, bool first) {
+template <int kH>
+__device__ __forceinline__ void issue_pvt(uint32_t tmem, uint32_t dhi, uint32_t p_hi, int t, uint32_t v_lo, uint32_t p_lo, bool first) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, kFew, true, false);
 #pragma unroll
     for (int kk = 0; kk < kBN / 16; ++kk)
-        umma_ss(tmem + kColO + t * 128, smem_desc_join(v_lo + (uint32_t)((kk * 2048) >> 4), dhi),
-                smem_desc_join(p_lo + (uint32_t)(((kk >> 2) * kFew * 128 + (kk & 3) * 32) >> 4), dhi), idesc,
+        umma_ss(tmem + kColO + t * 128, smem_desc_join(v_lo + (uint32_t)((kk * 2 * kH * kPart) >> 4), dhi),
+                smem_desc_join(p_lo + (uint32_t)(((kk >> 2) * kFew * 128 + (kk & 3) * 32) >> 4), p_hi), idesc,
                 first && kk == 0 ? 0u : 1u);
 }
 
@@ -476,25 +479,25 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
 
 // Copies rows of 64 kH elements (of which d exist, the others zeros) to a 128-byte
 // swizzled tile, 16 bytes a lane, whole rows of adjacent lanes.  at: the rows'
-// indexes in shared memory, -1 for a row of zeros; half: bytes between its 64-element parts.
+// indexes in shared memory, -1 for a row of zeros.
 template <int kH, int kUnroll>
-__device__ __forceinline__ void copy_rows(uint32_t tile, uint32_t half, const bf16* base, int64_t stride, const int32_t* at, int rows, int d) {
+__device__ __forceinline__ void copy_rows(uint32_t tile, const bf16* base, int64_t stride, const int32_t* at, int rows, int d) {
     constexpr int kPer = 4 / kH;  // rows a copy
     const int lane = threadIdx.x & 31, sub = lane / (8 * kH), c = lane % (8 * kH);
-    const uint32_t dst = tile + (c >> 3) * half + sub * 128;
+    const uint32_t dst = tile + (c >> 3) * kPart + sub * 128;
     const bool in = kH == 2 || c * 8 < d;
     const bf16* src = base + c * 8;
 #pragma unroll kUnroll
     for (int r = 0; r < rows; r += kPer) {
         const int from = at[r + sub];
         const bool on = from >= 0 && in;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((c & 7) ^ ((r + sub) & 7)) << 4)),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (r >> 3) * kH * kPart + (r & 7) * 128 + (((c & 7) ^ ((r + sub) & 7)) << 4)),
                      "l"(on ? src + from * stride : base), "r"(on ? 16 : 0)
                      : "memory");
     }
 }
 
-// kGather: pages of fewer than 16 rows, fetched row by row.
+// kGather: small pages, fetched row by row.
 template <int kH, bool kGather>
 __global__ void __launch_bounds__(Split<kGather>::kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -553,7 +556,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         const int quarter = kGather ? warp - 12 : 0;
         const int shift = u.page_shift;
         const int box_rows = shift >= 7 ? kBN : 1 << shift;
-        const int boxes = kBN / box_rows;  // per tile and 64-element part
+        const int boxes = kBN / box_rows;  // per tile
         Ring<kStages> ring(few_first);
         int issued = 0;       // steps of this kind
         bool k_pending = false, turned = false;
@@ -586,8 +589,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                     __syncwarp();
                     sm.kv_row[quarter][lane] = on ? (int)chunk_cache_row(u, it.b, key) : -1;
                     __syncwarp();
-                } else if (lane < kH * boxes) {
-                    const int key = it.key(x0 + (lane / kH) * box_rows);
+                } else if (lane < boxes) {
+                    const int key = it.key(x0 + lane * box_rows);
                     const bool on = key < it.hi && (key + box_rows > it.lo || key < u.sinks);
                     page = u.num_pages;  // outside the pool: zeros
                     in_page = key & ((1 << shift) - 1);
@@ -595,16 +598,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 }
                 auto load = [&](const CUtensorMap* map, const bf16* pages, uint64_t* bar, uint8_t* dst) {
                     if constexpr (kGather) {
-                        copy_rows<kH, 4>(smem_u32(dst) + quarter * 32 * 128, kHalf, pages + (int64_t)it.q * d, (int64_t)u.g * d,
+                        copy_rows<kH, 4>(smem_u32(dst) + quarter * 4 * kH * kPart, pages + (int64_t)it.q * d, (int64_t)u.g * d,
                                          sm.kv_row[quarter], kBN / 4, d);
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
                     } else {
                         if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
                         __syncwarp();
-                        if (lane < kH * boxes) {
-                            const int half = lane % kH;
-                            tma_load_4d(map, bar, dst + half * kHalf + (lane / kH) * box_rows * 128, half * 64, it.q, in_page, page);
-                        }
+                        if (lane < boxes)
+                            tma_load_5d(map, bar, dst + lane * (box_rows >> 3) * kH * kPart, 0, 0, 0, it.q,
+                                        (page << (shift - 3)) + (in_page >> 3));
                     }
                 };
                 // the second kind's stages lie in the first's memory
@@ -631,7 +633,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: S
         if (lane == 0) {
-            const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
+            const uint32_t dhi = smem_desc_hi(kH * kPart, kSwizzle128B);
             const uint32_t q_lo0 = smem_desc_lo(smem_u32(sm.q(0)), 16), q_lo1 = smem_desc_lo(smem_u32(sm.q(1)), 16);
             const uint32_t qf_lo = smem_desc_lo(smem_u32(sm.qf[0]), 16);
             Ring<kStages> ring(few_first);
@@ -767,7 +769,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const int buf = few_it & 1;
                 if (!warp_wait(sm, &sm.q_empty[buf], ((few_it >> 1) & 1) ^ 1, 21)) { ok = false; break; }
                 ++few_it;
-                copy_rows<kH, 4>(smem_u32(sm.qf[buf]), kFew * 128, p.Q, d, sm.row[slot][0], kFew, d);
+                copy_rows<kH, 4>(smem_u32(sm.qf[buf]), p.Q, d, sm.row[slot][0], kFew, d);
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();  // from the generic to the tensor cores' view
                 warp_arrive(&sm.q_full[buf]);
@@ -776,8 +778,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
     } else if (warp == 3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<kGather>::kRegsCtl));
         // ------------------------------------------------------------ MMA issuer: O += P V
-        const uint32_t dhi = smem_desc_hi(1024, kSwizzle128B);
-        const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v(0)), kH == 2 ? kHalf : 0);
+        const uint32_t dhi = smem_desc_hi(kH * kPart, kSwizzle128B);
+        const uint32_t p_hi = smem_desc_hi(kPart, kSwizzle128B);
+        const uint32_t v_lo0 = smem_desc_lo(smem_u32(sm.v(0)), kH == 2 ? kPart : 0);
         const uint32_t p_lo0 = smem_desc_lo(smem_u32(sm.p[0]), 16), p_lo1 = smem_desc_lo(smem_u32(sm.p[1]), 16);
         const int page = 1 << u.page_shift;
         Ring<kStages> ring(few_first);
@@ -814,9 +817,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         a = max(a, x0);
                         b = min(b, x1);
 #pragma unroll 1
-                        for (int x = lane; x < (b - a) * 8 * kH; x += 32)
-                            *reinterpret_cast<uint4*>(v + (kH == 2 && (x & 8) ? kHalf : 0) + (a - x0 + x / (8 * kH)) * 128 +
+                        for (int x = lane; x < (b - a) * 8 * kH; x += 32) {
+                            const int r = a - x0 + x / (8 * kH);
+                            *reinterpret_cast<uint4*>(v + ((r >> 3) * kH + (kH == 2 && (x & 8) ? 1 : 0)) * kPart + (r & 7) * 128 +
                                                       (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
                     };
                     zero(it.hi - it.skip, ((it.hi + page - 1) & ~(page - 1)) - it.skip);
                     if (u.window) {
@@ -836,7 +841,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                         tc_fence_after();
                         const uint32_t v_lo = v_lo0 + st * (kTileBytes >> 4);
                         if (few)
-                            issue_pvt(tmem, dhi, t, v_lo, t ? p_lo1 : p_lo0, j == 0);
+                            issue_pvt<kH>(tmem, dhi, p_hi, t, v_lo, t ? p_lo1 : p_lo0, j == 0);
                         else
                             issue_pv<kH>(tmem, dhi, t, v_lo, j == 0);
                         umma_commit(&sm.p_empty[t]);
@@ -931,7 +936,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         }
         // This warp's rows of an item's Q tile, in flight until q_ready.
         auto load_q = [&](int slot) {
-            copy_rows<kH, 4>(smem_u32(sm.q(t)) + wq * 32 * 128, kHalf, p.Q, d, sm.row[slot][t] + wq * 32, 32, d);
+            copy_rows<kH, 4>(smem_u32(sm.q(t)) + wq * 4 * kH * kPart, p.Q, d, sm.row[slot][t] + wq * 32, 32, d);
         };
         auto q_ready = [&]() {
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1263,19 +1268,20 @@ cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a, const CUtensorM
 cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a) {
     const gqe_shape& s = *a.s;
     const int page = 1 << a.page_shift;
-    // Pages of 16 rows or more by the TMA, a box per page and 64-element part; of
-    // fewer rows by copies, row by row: at 8 rows a page the boxes' number held 64
-    // decodes at 3.8 TB/s (16 rows: 5.8), at 4 rows the TMA's gather of four rows at a
-    // time at 1.9.
-    const bool gather = page < 16;
+    // A box per page of the TMA, or for smaller pages copies, row by row.  64 decodes of
+    // 1000 to 8000 keys, pages of 8 rows: d_h = 128, 213 us by boxes and 315 by copies;
+    // d_h = 64, whose boxes are half as large, 207 and 186.  16 rows: boxes, 189 and 165.
+    const bool gather = page < (s.d_h == 128 ? 8 : 16);
     CUtensorMap mapK{}, mapV{};
     if (!gather) {
         const uint64_t row_bytes = (uint64_t)s.d_h * 2;
-        const uint64_t dims[4] = {(uint64_t)s.d_h, (uint64_t)s.g, (uint64_t)page, (uint64_t)a.num_pages};
-        const uint64_t strides[3] = {row_bytes, s.g * row_bytes, (uint64_t)page * s.g * row_bytes};
-        const uint32_t box[4] = {64, 1, (uint32_t)(page < kBN ? page : kBN), 1};
-        if (!make_bf16_map(&mapK, a.K_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
-        if (!make_bf16_map(&mapV, a.V_pages, 4, dims, strides, box)) return cudaErrorInvalidValue;
+        const int parts = s.d_h == 128 ? 2 : 1;
+        // 64 elements, 8 rows, parts, groups, 8-row groups of the pool
+        const uint64_t dims[5] = {(uint64_t)(s.d_h / parts), 8, (uint64_t)parts, (uint64_t)s.g, (uint64_t)a.num_pages * page / 8};
+        const uint64_t strides[4] = {s.g * row_bytes, 128, row_bytes, 8 * s.g * row_bytes};
+        const uint32_t box[5] = {64, 8, (uint32_t)parts, 1, (uint32_t)(page < kBN ? page : kBN) / 8};
+        if (!make_bf16_map(&mapK, a.K_pages, 5, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!make_bf16_map(&mapV, a.V_pages, 5, dims, strides, box)) return cudaErrorInvalidValue;
     }
     if (s.d_h == 128) return gather ? launch_typed<2, true>(u, a, mapK, mapV) : launch_typed<2, false>(u, a, mapK, mapV);
     return gather ? launch_typed<1, true>(u, a, mapK, mapV) : launch_typed<1, false>(u, a, mapK, mapV);
