@@ -8,19 +8,24 @@ namespace {
 // After the tile kernel, block c, of either kind of units:
 //  1. takes again the rows of CTA c's whole units whose result is not finite (only
 //     if the CTA has flagged one): see chunk_row;
-//  2. merges the split unit whose first steps part c holds as its last:
-//     O = gate * sum_p 2^(lse_p - M) o_p / sum_p 2^(lse_p - M) over its parts in
-//     order (reproducible).
+//  2. merges its share of the split units that part c has steps of, its last and its
+//     first: O = gate * sum_p 2^(lse_p - M) o_p / sum_p 2^(lse_p - M) over a unit's
+//     parts in order (reproducible).  The blocks of a unit's parts take its groups of
+//     kRows rows in turn (by the block of its first part alone, 64 prompt units in two
+//     to four parts each kept 64 of 148 blocks busy, for 20 us).
 // One block per part: with blocks by part and row range, most of them with nothing
 // to do, 20 us went by on their starting and leaving.
 constexpr int kCombineWarps = 16;
+constexpr int kRows = 4;  // rows a warp merges at once
 
-// The rows of a unit whose result is not finite from the formula, a warp each.
+// The rows of a unit, of a share of its groups of kRows rows, whose result is not
+// finite from the formula, a warp each.
 template <typename T, int D>
-__device__ __noinline__ void unit_again(const ChunkGeom& u, const ChunkItem& it, int warp, const T* Q, const T* Kp,
-                                        const T* Vp, float scale_log2, T* O) {
+__device__ __noinline__ void unit_again(const ChunkGeom& u, const ChunkItem& it, int share, int shares, int warp, const T* Q,
+                                        const T* Kp, const T* Vp, float scale_log2, T* O) {
     const int lane = threadIdx.x & 31;
     for (int r = warp; r < it.nt * u.k; r += kCombineWarps) {
+        if (r / kRows % shares != share) continue;
         const int token = it.t0 + r / u.k;
         const int64_t at = ((int64_t)token * u.g + it.q) * u.k + r % u.k;
         const int j = u.idx[at];
@@ -67,37 +72,61 @@ template <typename T, int D>
 __global__ void __launch_bounds__(32 * kCombineWarps, 1)
 chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
                      float scale_log2, T* __restrict__ O) {
-    constexpr int kRec = D + 4, kPer = D / 32, kRows = 4;
-    __shared__ int list[2][kChunkMaxParts];  // by kind: the unit's records in order
-    __shared__ int count[2];
-    __shared__ ChunkDesc desc[2];
+    constexpr int kRec = D + 4, kPer = D / 32;
+    // By kind and, below it, the part's last unit and its first: the unit, its records
+    // in order and this block's share of its rows.
+    __shared__ int list[4][2 * kChunkMaxParts];  // the block's own part at kChunkMaxParts
+    __shared__ int from[4], count[4], share[4];
+    __shared__ ChunkDesc desc[4];
     __shared__ ChunkSplit split;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool odd = false;
-    if (warp < 2) {  // warp `kind` finds the unit and its parts
-        const int c = warp * u.parts + blockIdx.x, end = (warp + 1) * u.parts;
-        const ChunkDesc d = u.desc[2 * c + 1];
-        odd = lane == 0 && u.odd[c] != 0;
-        int n = d.valid ? 1 : 0;
-        for (int p0 = c + 1; p0 < end; p0 += 32) {
-            const int p = p0 + lane;
-            bool mine = false, other = p >= end;
-            ChunkDesc e;
-            if (p < end) {
-                e = u.desc[2 * p];  // in flight with d
-                mine = d.valid && e.valid && e.q == d.q && e.t0 == d.t0 && e.b == d.b;
-                other = e.valid && !mine;
+    if (warp < 4) {
+        const int kind = warp >> 1, first = warp & 1, begin = kind * u.parts, end = begin + u.parts, c = begin + blockIdx.x;
+        // The first rounds' loads are in flight together, 32 parts back and ahead.
+        const ChunkDesc none = {-1, 0, 0, 0};
+        auto at = [&](int p, int last) {
+            const bool in = p >= begin && p < end;
+            int4 v = make_int4(-1, 0, 0, 0);
+            if (in) v = *reinterpret_cast<const int4*>(&u.desc[2 * p + last]);
+            return ChunkDesc{v.x, v.y, v.z, v.w};
+        };
+        const ChunkDesc d = at(c, 1 - first);
+        ChunkDesc middle = first ? at(c - 1 - lane, 0) : none, start = first ? at(c - 1 - lane, 1) : none, ahead = at(c + 1 + lane, 0);
+        odd = lane == 0 && !first && u.odd[c] != 0;
+        int before = 0, after = 1;
+        if (first && d.b >= 0) {  // the parts back to the one that has the unit as its last
+            for (int p0 = c - 1;;) {
+                const unsigned starts = __ballot_sync(0xffffffffu, start.same_unit(d));
+                const unsigned in = __ballot_sync(0xffffffffu, start.same_unit(d) || middle.same_unit(d)) &
+                                    (starts ? 2u * (starts & -starts) - 1u : 0xffffffffu);
+                if (in >> lane & 1)
+                    list[warp][kChunkMaxParts - 1 - before - __popc(in & ((1u << lane) - 1u))] = start.same_unit(d) ? start.rec : middle.rec;
+                before += __popc(in);
+                p0 -= 32;
+                if (starts || p0 < begin) break;
+                middle = at(p0 - lane, 0);
+                start = at(p0 - lane, 1);
             }
-            const unsigned in = __ballot_sync(0xffffffffu, mine), out = __ballot_sync(0xffffffffu, other);
-            if (mine) list[warp][n + __popc(in & ((1u << lane) - 1u))] = e.rec;
-            n += __popc(in);
-            if (out || !d.valid) break;  // a later unit's part: this unit's are all behind
+        }
+        if (d.b >= 0) {
+            for (int p0 = c + 1;;) {
+                const unsigned in = __ballot_sync(0xffffffffu, ahead.same_unit(d));
+                const unsigned out = __ballot_sync(0xffffffffu, ahead.b >= 0 && !ahead.same_unit(d));
+                if (in >> lane & 1) list[warp][kChunkMaxParts + after + __popc(in & ((1u << lane) - 1u))] = ahead.rec;
+                after += __popc(in);
+                p0 += 32;
+                if (out || p0 >= end) break;  // a later unit's part: this unit's are all behind
+                ahead = at(p0 + lane, 0);
+            }
         }
         if (lane == 0) {
-            list[warp][0] = d.rec;
-            count[warp] = n;
+            list[warp][kChunkMaxParts] = d.rec;
+            from[warp] = kChunkMaxParts - before;
+            count[warp] = d.b >= 0 ? before + after : 0;
+            share[warp] = before;
             desc[warp] = d;
         }
     }
@@ -109,86 +138,102 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
             ChunkWalk walk(u, split, kind, blockIdx.x);
             ChunkItem it;
             while (walk.next(u, it, false))
-                if (it.rec < 0) unit_again<T, D>(u, it, warp, Q, Kp, Vp, scale_log2, O);
+                if (it.rec < 0) unit_again<T, D>(u, it, 0, 1, warp, Q, Kp, Vp, scale_log2, O);
             __syncthreads();  // split may be overwritten
         }
     }
-    bool bad[2] = {false, false};
+    bool bad = false;
+    // The warp's groups of rows, unit by unit; the next group's heads and gates are on
+    // their way while a group is merged.
+    int set = -1, group = 0, to[kRows];
+    float gate[kRows];
+    auto next = [&]() {
+        if (set >= 0) group += count[set] * kCombineWarps;
+        while (set < 0 || group * kRows >= (count[set] ? desc[set].nt() * u.k : 0)) {
+            if (++set == 4) return;
+            group = share[set] + count[set] * warp;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const ChunkDesc& d = desc[set];
+            const int r = min(group * kRows + i, d.nt() * u.k - 1), token = r * u.inv_k >> 16;
+            const int64_t at = ((int64_t)(d.t0 + token) * u.g + d.q()) * u.k + r - token * u.k;
+            to[i] = u.idx[at];
+            gate[i] = u.gate[at];
+        }
+    };
+    next();
 #pragma unroll 1
-    for (int kind = 0; kind < 2; ++kind) {
-        const int n = count[kind], rows = n ? desc[kind].nt * u.k : 0;
-        for (int r0 = warp * kRows; r0 < rows; r0 += kCombineWarps * kRows) {
-            const ChunkDesc& d = desc[kind];
-            // kRows rows and two parts at once, all their loads in flight together (with
-            // the maxima in a pass of their own, and a row's loads after another's, 45 us
-            // for 38 MB of records); lane holds elements kPer * lane ..  The running
-            // maximum, sum and row take the parts in order.
-            int to[kRows];  // the row of O, or -1
-            float gate[kRows], M[kRows], L[kRows], acc[kRows][kPer];
+    while (set < 4) {
+        const ChunkDesc& d = desc[set];
+        const int n = count[set], rows = d.nt() * u.k, r0 = group * kRows;
+        const int* recs = list[set] + from[set];
+        // kRows rows and two parts at once, all their loads in flight together (with
+        // the maxima in a pass of their own, and a row's loads after another's, 45 us
+        // for 38 MB of records); lane holds elements kPer * lane ..  The running
+        // maximum, sum and row take the parts in order.
+        int row[kRows];  // of O, or -1
+        float f[kRows], M[kRows], L[kRows], acc[kRows][kPer];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int r = min(r0 + i, rows - 1), token = d.t0 + (r * u.inv_k >> 16);
-                const int64_t at = ((int64_t)token * u.g + d.q) * u.k + r - (r * u.inv_k >> 16) * u.k;
-                to[i] = u.idx[at];
-                gate[i] = u.gate[at];
-                M[i] = -INFINITY;
-                L[i] = 0.f;
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i;
+            const bool in = r < rows && to[i] >= d.q() * u.hpg && to[i] < (d.q() + 1) * u.hpg;
+            row[i] = in ? (d.t0 + (r * u.inv_k >> 16)) * u.h + to[i] : -1;
+            f[i] = gate[i];
+            M[i] = -INFINITY;
+            L[i] = 0.f;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
-            }
-            for (int p = 0; p < n; p += 2) {
-                float lse[2][kRows], v[2][kRows][kPer];
+            for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
+        }
+        next();
+#pragma unroll 1
+        for (int p = 0; p < n; p += 2) {
+            float lse[2][kRows], v[2][kRows][kPer];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float* rec0 = u.part + (int64_t)list[kind][min(p + x, n - 1)] * kRec;
-#pragma unroll
-                    for (int i = 0; i < kRows; ++i) {
-                        const float* rec = rec0 + min(r0 + i, rows - 1) * kRec;
-                        lse[x][i] = p + x < n ? rec[D] : -INFINITY;
-                        load_lane(rec + lane * kPer, v[x][i]);
-                    }
-                }
+            for (int x = 0; x < 2; ++x) {
+                const float* rec0 = u.part + (int64_t)recs[min(p + x, n - 1)] * kRec;
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
-                    // a log-sum-exp of -inf: no key of the row in that part
-                    const float m = fmaxf(fmaxf(lse[0][i], lse[1][i]), M[i]), ref = m == -INFINITY ? 0.f : m;
-                    const float w = fast_exp2(M[i] - ref), a = fast_exp2(lse[0][i] - ref), b = fast_exp2(lse[1][i] - ref);
-                    M[i] = m;
-                    L[i] = L[i] * w + a + b;
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e)
-                        acc[i][e] = acc[i][e] * w + (lse[0][i] == -INFINITY ? 0.f : v[0][i][e] * a) +
-                                    (lse[1][i] == -INFINITY ? 0.f : v[1][i][e] * b);
+                    const float* rec = rec0 + min(r0 + i, rows - 1) * kRec;
+                    lse[x][i] = p + x < n ? rec[D] : -INFINITY;
+                    load_lane(rec + lane * kPer, v[x][i]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                const int r = r0 + i;
-                const bool in = r < rows && to[i] >= d.q * u.hpg && to[i] < (d.q + 1) * u.hpg;
-                to[i] = in ? (d.t0 + (r * u.inv_k >> 16)) * u.h + to[i] : -1;
-            }
+                // a log-sum-exp of -inf: no key of the row in that part
+                const float m = fmaxf(fmaxf(lse[0][i], lse[1][i]), M[i]), ref = m == -INFINITY ? 0.f : m;
+                const float w = fast_exp2(M[i] - ref), a = fast_exp2(lse[0][i] - ref), b = fast_exp2(lse[1][i] - ref);
+                M[i] = m;
+                L[i] = L[i] * w + a + b;
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (to[i] < 0) continue;
-                const float f = gate[i] / L[i];
-                float check = L[i] * 0.f;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    check += acc[i][e] * 0.f;
-                    acc[i][e] *= f;
-                }
-                if (!(check == 0.f)) bad[kind] = true;
-                store_lane(O + (int64_t)to[i] * D + lane * kPer, acc[i]);
+                for (int e = 0; e < kPer; ++e)
+                    acc[i][e] = acc[i][e] * w + (lse[0][i] == -INFINITY ? 0.f : v[0][i][e] * a) +
+                                (lse[1][i] == -INFINITY ? 0.f : v[1][i][e] * b);
             }
         }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (row[i] < 0) continue;
+            const float scale = f[i] / L[i];
+            float check = L[i] * 0.f;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                check += acc[i][e] * 0.f;
+                acc[i][e] *= scale;
+            }
+            if (!(check == 0.f)) bad = true;
+            store_lane(O + (int64_t)row[i] * D + lane * kPer, acc[i]);
+        }
     }
-    for (int kind = 0; kind < 2; ++kind) {
-        if (!__syncthreads_or(kind ? bad[1] : bad[0])) continue;
-        const ChunkDesc d = desc[kind];
+    if (!__syncthreads_or(bad)) return;
+    for (int x = 0; x < 4; ++x) {
+        if (!count[x]) continue;
+        const ChunkDesc d = desc[x];
         const ChunkSeq s = chunk_seq(u, d.b);
         ChunkItem it;
-        chunk_item(u, s, d.b, d.q, (d.t0 - s.t0) / u.WU, it);
-        unit_again<T, D>(u, it, warp, Q, Kp, Vp, scale_log2, O);
+        chunk_item(u, s, d.b, d.q(), (d.t0 - s.t0) / u.WU, it);
+        unit_again<T, D>(u, it, share[x], count[x], warp, Q, Kp, Vp, scale_log2, O);
     }
 }
 

@@ -34,8 +34,13 @@ constexpr int kChunkMaxParts = 512;        // grid limit of the chunk kernels
 constexpr uint32_t kWhereChunk = 8;        // status "where" id of the chunk kernels
 
 // One partial unit: what the merge needs to find its rows.
-struct ChunkDesc {
-    int32_t valid, b, q, t0, nt, rec;
+struct __align__(16) ChunkDesc {
+    int32_t b, t0, q_nt, rec;  // b: -1 when there is none; q_nt: group << 16 | tokens
+    __device__ __forceinline__ int q() const { return q_nt >> 16; }
+    __device__ __forceinline__ int nt() const { return q_nt & 0xffff; }
+    __device__ __forceinline__ bool same_unit(const ChunkDesc& o) const {
+        return b >= 0 && b == o.b && t0 == o.t0 && q_nt == o.q_nt;
+    }
 };
 
 struct ChunkGeom {
@@ -329,7 +334,7 @@ struct ChunkWalk {
         if (it.s0 > 0 || it.s1 < it.steps) {
             const int slot = it.s0 > 0 ? 2 * part : 2 * part + 1;
             it.rec = kind ? 2 * u.parts * u.row_cap + slot * u.few_cap : slot * u.row_cap;
-            if ((threadIdx.x & 31) == 0 && describe) u.desc[kind * 2 * u.parts + slot] = {1, it.b, it.q, it.t0, it.nt, it.rec};
+            if ((threadIdx.x & 31) == 0 && describe) u.desc[kind * 2 * u.parts + slot] = {it.b, it.t0, it.q << 16 | it.nt, it.rec};
         }
         ++at.i;
         at.s = 0;
@@ -347,7 +352,7 @@ __device__ __forceinline__ bool chunk_has(const ChunkGeom& u, const ChunkSplit& 
 __device__ __forceinline__ void chunk_clear(const ChunkGeom& u) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        u.desc[(i >> 1) * 2 * u.parts + 2 * chunk_part(u, i >> 1, blockIdx.x) + (i & 1)].valid = 0;
+        u.desc[(i >> 1) * 2 * u.parts + 2 * chunk_part(u, i >> 1, blockIdx.x) + (i & 1)].b = -1;
     u.odd[blockIdx.x] = u.odd[u.parts + blockIdx.x] = 0;
 }
 
