@@ -502,8 +502,8 @@ gqe_status gqe_aux_loss(const gqe_shape* s, const float* logits, const int32_t* 
  *   slots [rows]         device int32 out: page * page_size + row in page of each
  *                        packed row, -1 for the padding; may be NULL if rows is 0
  *   workspace            the status word (256 bytes)
- * lengths and free_count are not written, so a repeated call with the same
- * arguments gives the same result; the caller passes lengths_out and
+ * lengths and free_count are not written (lengths_out and free_count_out must be
+ * other memory), so a repeated call with the same arguments gives the same result; the caller passes lengths_out and
  * free_count_out to the next step.  A step that cannot be served is refused as
  * a whole: GQE_ERR_OUT_OF_PAGES in the status word if the free pages do not
  * suffice, GQE_ERR_INVALID_ARGUMENT for a negative length, new_lens below -1, a
@@ -555,7 +555,8 @@ gqe_status gqe_kv_append(const gqe_shape* s, const void* K_new, int64_t k_stride
  *   s                B must be 1, T = the rows of Q, idx, gate and O
  *   Q, O [T, h, d_h], idx, gate [T, g, k] as for gqe_attn_prefill; a head outside
  *                    its group is reported in the status word and its row skipped
- *                    (a token's heads must differ, as the router picks them)
+ *                    (a token's heads must differ, as the router picks them; O is
+ *                    other memory than Q)
  *   K_pages, V_pages, num_pages, page_size, block_table, max_blocks
  *                    as for gqe_attn_decode_paged; page_size * max_blocks <= 2^30
  *   cu_new [n_seqs + 1], lengths [n_seqs]   device int32: as gqe_page_plan writes

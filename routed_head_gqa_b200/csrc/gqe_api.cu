@@ -13,6 +13,12 @@ namespace {
 constexpr int kMaxK = 16;
 constexpr int kMaxH = 256;
 
+// Whether two arrays of n entries share one.
+bool overlap(const int32_t* a, const int32_t* b, int64_t n) {
+    const int64_t d = reinterpret_cast<intptr_t>(a) - reinterpret_cast<intptr_t>(b);
+    return d < 4 * n && -d < 4 * n;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 gqe_status check_shape(const gqe_shape* s) {
@@ -432,6 +438,8 @@ gqe_status gqe_page_plan(int n_seqs, int rows, int page_size, int num_pages, int
         return GQE_ERR_UNSUPPORTED;
     gqe_status st = check_workspace(workspace, workspace_bytes, kStatusBytes);
     if (st != GQE_OK) return st;
+    // Every block reads the state before the step while others write the state after it.
+    if (overlap(lengths, lengths_out, n_seqs) || overlap(free_count, free_count_out, 1)) return GQE_ERR_INVALID_ARGUMENT;
     PlanArgs a;
     a.n_seqs = n_seqs;
     a.rows = rows;

@@ -37,6 +37,14 @@ def test_plan_refuses(g, change, code):
     assert g._lib.gqe_page_plan(*{**PLAN, **change}.values(), None) == code
 
 
+@pytest.mark.parametrize("change", [dict(lengths_out=FAKE), dict(lengths_out=FAKE + 12), dict(lengths=FAKE + 0x1000 + 12),
+                                    dict(free_count_out=FAKE)])
+def test_plan_refuses_state_in_place(g, change):
+    """The state after the step in the memory of the state before it."""
+    apart = dict(lengths_out=FAKE + 0x1000, free_count_out=FAKE + 0x2000)
+    assert g._lib.gqe_page_plan(*{**PLAN, **apart, **change}.values(), None) == 1
+
+
 @pytest.mark.parametrize("change,code", [
     *[({name: None}, 1) for name in ("K_new", "V_new", "slots", "K_pages", "V_pages", "workspace")],
     (dict(K_new=FAKE + 8), 1), (dict(V_pages=FAKE + 4), 1), (dict(num_pages=0), 1), (dict(page_size=3), 1),
