@@ -143,87 +143,71 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
         }
     }
     bool bad = false;
-    // The warp's groups of rows, unit by unit; the next group's heads and gates are on
-    // their way while a group is merged.
-    int set = -1, group = 0, to[kRows];
-    float gate[kRows];
-    auto next = [&]() {
-        if (set >= 0) group += count[set] * kCombineWarps;
-        while (set < 0 || group * kRows >= (count[set] ? desc[set].nt() * u.k : 0)) {
-            if (++set == 4) return;
-            group = share[set] + count[set] * warp;
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const ChunkDesc& d = desc[set];
-            const int r = min(group * kRows + i, d.nt() * u.k - 1), token = r * u.inv_k >> 16;
-            const int64_t at = ((int64_t)(d.t0 + token) * u.g + d.q()) * u.k + r - token * u.k;
-            to[i] = u.idx[at];
-            gate[i] = u.gate[at];
-        }
-    };
-    next();
 #pragma unroll 1
-    while (set < 4) {
+    for (int set = 0; set < 4; ++set) {
         const ChunkDesc& d = desc[set];
-        const int n = count[set], rows = d.nt() * u.k, r0 = group * kRows;
+        const int n = count[set], rows = n ? d.nt() * u.k : 0;
         const int* recs = list[set] + from[set];
-        // kRows rows and two parts at once, all their loads in flight together (with
-        // the maxima in a pass of their own, and a row's loads after another's, 45 us
-        // for 38 MB of records); lane holds elements kPer * lane ..  The running
-        // maximum, sum and row take the parts in order.
-        int row[kRows];  // of O, or -1
-        float f[kRows], M[kRows], L[kRows], acc[kRows][kPer];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i;
-            const bool in = r < rows && to[i] >= d.q() * u.hpg && to[i] < (d.q() + 1) * u.hpg;
-            row[i] = in ? (d.t0 + (r * u.inv_k >> 16)) * u.h + to[i] : -1;
-            f[i] = gate[i];
-            M[i] = -INFINITY;
-            L[i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
-        }
-        next();
 #pragma unroll 1
-        for (int p = 0; p < n; p += 2) {
-            float lse[2][kRows], v[2][kRows][kPer];
+        for (int r0 = (share[set] + n * warp) * kRows; r0 < rows; r0 += n * kCombineWarps * kRows) {
+            // kRows rows and two parts at once, all their loads in flight together (with
+            // the maxima in a pass of their own, and a row's loads after another's, 45 us
+            // for 38 MB of records); lane holds elements kPer * lane ..  The running
+            // maximum, sum and row take the parts in order.
+            int to[kRows];  // the head
+            float gate[kRows], M[kRows], L[kRows], acc[kRows][kPer];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float* rec0 = u.part + (int64_t)recs[min(p + x, n - 1)] * kRec;
+            for (int i = 0; i < kRows; ++i) {
+                const int r = min(r0 + i, rows - 1), token = r * u.inv_k >> 16;
+                const int64_t at = ((int64_t)(d.t0 + token) * u.g + d.q()) * u.k + r - token * u.k;
+                to[i] = u.idx[at];  // first used behind the loop, so that the records' loads follow at once
+                gate[i] = u.gate[at];
+                M[i] = -INFINITY;
+                L[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
+            }
+#pragma unroll 1
+            for (int p = 0; p < n; p += 2) {
+                float lse[2][kRows], v[2][kRows][kPer];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float* rec0 = u.part + (int64_t)recs[min(p + x, n - 1)] * kRec;
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+                        const float* rec = rec0 + min(r0 + i, rows - 1) * kRec;
+                        lse[x][i] = p + x < n ? rec[D] : -INFINITY;
+                        load_lane(rec + lane * kPer, v[x][i]);
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
-                    const float* rec = rec0 + min(r0 + i, rows - 1) * kRec;
-                    lse[x][i] = p + x < n ? rec[D] : -INFINITY;
-                    load_lane(rec + lane * kPer, v[x][i]);
+                    // a log-sum-exp of -inf: no key of the row in that part
+                    const float m = fmaxf(fmaxf(lse[0][i], lse[1][i]), M[i]), ref = m == -INFINITY ? 0.f : m;
+                    const float w = fast_exp2(M[i] - ref), a = fast_exp2(lse[0][i] - ref), b = fast_exp2(lse[1][i] - ref);
+                    M[i] = m;
+                    L[i] = L[i] * w + a + b;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e)
+                        acc[i][e] = acc[i][e] * w + (lse[0][i] == -INFINITY ? 0.f : v[0][i][e] * a) +
+                                    (lse[1][i] == -INFINITY ? 0.f : v[1][i][e] * b);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                // a log-sum-exp of -inf: no key of the row in that part
-                const float m = fmaxf(fmaxf(lse[0][i], lse[1][i]), M[i]), ref = m == -INFINITY ? 0.f : m;
-                const float w = fast_exp2(M[i] - ref), a = fast_exp2(lse[0][i] - ref), b = fast_exp2(lse[1][i] - ref);
-                M[i] = m;
-                L[i] = L[i] * w + a + b;
+                const int r = r0 + i;
+                if (r >= rows || to[i] < d.q() * u.hpg || to[i] >= (d.q() + 1) * u.hpg) continue;
+                const int64_t row = (int64_t)(d.t0 + (r * u.inv_k >> 16)) * u.h + to[i];
+                const float scale = gate[i] / L[i];
+                float check = L[i] * 0.f;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    acc[i][e] = acc[i][e] * w + (lse[0][i] == -INFINITY ? 0.f : v[0][i][e] * a) +
-                                (lse[1][i] == -INFINITY ? 0.f : v[1][i][e] * b);
+                for (int e = 0; e < kPer; ++e) {
+                    check += acc[i][e] * 0.f;
+                    acc[i][e] *= scale;
+                }
+                if (!(check == 0.f)) bad = true;
+                store_lane(O + row * D + lane * kPer, acc[i]);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (row[i] < 0) continue;
-            const float scale = f[i] / L[i];
-            float check = L[i] * 0.f;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                check += acc[i][e] * 0.f;
-                acc[i][e] *= scale;
-            }
-            if (!(check == 0.f)) bad = true;
-            store_lane(O + (int64_t)row[i] * D + lane * kPer, acc[i]);
         }
     }
     if (!__syncthreads_or(bad)) return;
@@ -248,11 +232,17 @@ size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
 
 bool on_tensor_cores(const gqe_shape* s) { return s->dtype == GQE_BF16; }
 
-ChunkTiling tiling(const gqe_shape* s) { return on_tensor_cores(s) ? chunk_tc_tiling() : chunk_simt_tiling(); }
+ChunkTiling tiling(const gqe_shape* s) { return on_tensor_cores(s) ? chunk_tc_tiling() : chunk_simt_tiling(s->d_h); }
 
 int max_parts(const ChunkTiling& t) {
     const int p = t.per_sm * device_sms();
     return p < kChunkMaxParts ? p : kChunkMaxParts;
+}
+
+// Units per group: no more than one per token, nor than the full ones and one per request.
+int64_t max_units(const gqe_shape& s, const ChunkTiling& t, int n_seqs) {
+    const int64_t full = (s.T + (int64_t)t.tiles * (t.rows / s.k) - 1) / (t.tiles * (t.rows / s.k)) + (int64_t)n_seqs;
+    return full < s.T ? full : s.T;
 }
 
 // Query rows of a unit: a step of few tokens cannot fill it.
@@ -293,9 +283,7 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     u.page_shift = a.page_shift;
     const int page = 1 << a.page_shift;
     u.align = page < 8 ? 8 : page < t.keys ? page : t.keys;
-    // No more than one unit per token, nor than the full ones and one per request.
-    int64_t units = (s.T + u.WU - 1) / u.WU + (int64_t)a.n_seqs;
-    if (units > s.T) units = s.T;
+    const int64_t units = max_units(s, t, a.n_seqs);
     u.unit_cost[0] = (float)t.unit_keys;
     u.unit_cost[1] = (float)t.few_keys;
     u.cost_scale = 1.0f / 16;
@@ -348,7 +336,12 @@ size_t chunk_scratch_bytes(const gqe_shape* s) {
 
 cudaError_t launch_chunk(const ChunkArgs& a) {
     const ChunkTiling t = tiling(a.s);
-    const int parts = max_parts(t);
+    // No more blocks than a step of this shape can give parts: idle ones cost small steps
+    // their starting and leaving.
+    const int64_t cap = (int64_t)a.max_blocks << a.page_shift, span = (int64_t)a.window + a.sinks + t.tiles * (t.rows / a.s->k);
+    const int64_t keys = (a.window && span < cap ? span : cap) + (t.unit_keys > t.few_keys ? t.unit_keys : t.few_keys);
+    const int64_t pieces = max_units(*a.s, t, a.n_seqs) * a.s->g * ((keys + t.min_keys - 1) / t.min_keys);
+    const int parts = pieces < max_parts(t) ? (int)pieces : max_parts(t);
     const ChunkGeom u = make_geom(a, t, parts);
     const cudaError_t err = on_tensor_cores(a.s) ? launch_chunk_tc(u, a) : launch_chunk_simt(u, a);
     if (err != cudaSuccess) return err;

