@@ -110,8 +110,10 @@ def _load():
 
 
 class _LazyLib:
-    def __getattr__(self, name):
-        return getattr(_load(), name)
+    def __getattr__(self, name):  # the first time: then the function is an attribute of its own
+        fn = getattr(_load(), name)
+        setattr(self, name, fn)
+        return fn
 
 
 _lib = _LazyLib()
@@ -132,9 +134,9 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:  # the current stream's handle (a torch Stream object costs 3 us to make)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -327,7 +329,7 @@ def gqe_page_plan(page_size, lengths, new_lens, free_pages, free_count, block_ta
     _check(fn, _lib.gqe_page_plan(
         n, rows, int(page_size), pages, blocks, lengths.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
         free_count.data_ptr(), block_table.data_ptr(), lengths_out.data_ptr(), free_count_out.data_ptr(),
-        cu_new.data_ptr(), slots.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
+        cu_new.data_ptr(), slots.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream, dev)))
 
 
 def _pages(fn, dev, shape, dtype, K_pages, V_pages):
@@ -358,7 +360,7 @@ def gqe_kv_append(shape, K_new, V_new, slots, K_pages, V_pages, workspace, strea
         strides.append(st[0])
     _check(fn, _lib.gqe_kv_append(ctypes.byref(shape), K_new.data_ptr(), strides[0], V_new.data_ptr(), strides[1],
                                   slots.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), pages, page_size,
-                                  workspace.data_ptr(), nbytes, _stream(stream)))
+                                  workspace.data_ptr(), nbytes, _stream(stream, dev)))
 
 
 def gqe_chunk_workspace_bytes(shape) -> int:
@@ -385,7 +387,7 @@ def gqe_attn_chunk_paged(shape, Q, K_pages, V_pages, block_table, cu_new, length
     _check(fn, _lib.gqe_attn_chunk_paged(
         ctypes.byref(shape), Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), pages, page_size,
         block_table.data_ptr(), blocks, n, cu_new.data_ptr(), lengths.data_ptr(), int(window), int(sinks),
-        idx.data_ptr(), gate.data_ptr(), O.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
+        idx.data_ptr(), gate.data_ptr(), O.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream, dev)))
 
 
 def gqe_get_device_status(workspace, stream=None) -> int:

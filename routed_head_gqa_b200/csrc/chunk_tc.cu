@@ -177,6 +177,15 @@ struct Params {
     int d;          // d_h
 };
 
+__device__ __forceinline__ void tma_load_5d(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1, int c2, int c3,
+                                            int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
 template <class S>
 __device__ __forceinline__ bool aborted(S& sm) { return *((volatile int32_t*)&sm.abort_flag) != 0; }
 // Bounded wait of at most kWaitTimeoutNs, in few instructions: the roles wait in

@@ -4,6 +4,7 @@
 
 #include "backward.cuh"
 #include "chunk.cuh"
+#include "paged.cuh"
 #include "common.cuh"
 
 using namespace gqe;

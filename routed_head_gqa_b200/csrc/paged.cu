@@ -1,7 +1,7 @@
 // paged.cu -- the paged KV cache of a serving step: block tables and slot maps
 // from the requests' lengths (gqe_page_plan), and the step's new K/V rows
 // written to their slots (gqe_kv_append).
-#include "common.cuh"
+#include "paged.cuh"
 
 namespace gqe {
 namespace {
