@@ -691,7 +691,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 const int qb = few ? few_it++ & 1 : 0;
                 const uint32_t q_lo = qf_lo + qb * (sizeof(sm.qf[0]) >> 4);
                 for (int t = 0; t < kQT && ok; ++t) {
-                    if (few ? t != qb : t > 0 && tiles < 2) continue;
+                    if (few ? t != qb : (t ? tiles < 2 || n1 == 0 : n0 == 0)) continue;
                     if (few) {
                         ok = bar_wait(&sm.q_full[t], (t ? q_use[1] : q_use[0]) & 1);
                         if (t) ++q_use[1]; else ++q_use[0];
@@ -982,8 +982,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
                 done();
                 continue;
             }
-            if (!loaded) load_q(slot);
-            q_ready();
+            // A tile without steps in this part (only a CTA's first unit has such) has no Q
+            // either: nobody would wait before the next unit's came.
+            if (n > 0) {
+                if (!loaded) load_q(slot);
+                q_ready();
+            }
             loaded = false;
             const bool partial = it.rec >= 0;
             const bool mine = in_tile && off < it.nt;

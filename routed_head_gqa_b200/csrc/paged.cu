@@ -110,7 +110,7 @@ page_plan_kernel(const PlanArgs a) {
             a.cu_new[b] = 0;
             if (b < n) a.lengths_out[b] = a.lengths[b];
         }
-        for (int t = gtid; t < a.rows; t += gsize) a.slots[t] = -1;
+        for (int64_t t = gtid; t < a.rows; t += gsize) a.slots[t] = -1;
         return;
     }
     for (int b = b0; b < b1; ++b) {
@@ -146,11 +146,11 @@ page_plan_kernel(const PlanArgs a) {
         report_error(a.status, GQE_ERR_INVALID_ARGUMENT, kWherePlan, 1);
         return false;
     };
-    for (int t = gtid; t < a.rows; t += gsize) {
+    for (int64_t t = gtid; t < a.rows; t += gsize) {
         int slot = -1;
         if (t < rows_at[n]) {
-            const int b = find_owner(rows_at, n, t);
-            const int pos = a.lengths[b] + (t - rows_at[b]), blk = pos >> a.page_shift, have = blocks_of(b);
+            const int b = find_owner(rows_at, n, (int)t);
+            const int pos = a.lengths[b] + ((int)t - rows_at[b]), blk = pos >> a.page_shift, have = blocks_of(b);
             const int page = blk < have ? a.block_table[(int64_t)b * a.max_blocks + blk] : pop(need_at[b] + blk - have);
             if (check(page)) slot = (page << a.page_shift) | (pos & (int)(ps - 1));
         }
