@@ -73,18 +73,20 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 1)
 chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ Q, const T* __restrict__ Kp, const T* __restrict__ Vp,
                      float scale_log2, T* __restrict__ O) {
     constexpr int kRec = D + 4, kPer = D / 32;
-    // By kind and, below it, the part's last unit and its first: the unit, its records
-    // in order and this block's share of its rows.
-    __shared__ int list[4][2 * kChunkMaxParts];  // the block's own part at kChunkMaxParts
-    __shared__ int from[4], count[4], share[4];
-    __shared__ ChunkDesc desc[4];
+    // The part's last units of many and few rows, and its first unit of many rows (a
+    // unit of few is a group or four of kRows: the block of its first part merges it
+    // alone): the unit, its records in order and this block's share of its groups.
+    constexpr int kSets = 3;
+    __shared__ int list[kSets][2 * kChunkMaxParts];  // the block's own part at kChunkMaxParts
+    __shared__ int from[kSets], count[kSets], share[kSets], shares[kSets];
+    __shared__ ChunkDesc desc[kSets];
     __shared__ ChunkSplit split;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool odd = false;
-    if (warp < 4) {
-        const int kind = warp >> 1, first = warp & 1, begin = kind * u.parts, end = begin + u.parts, c = begin + blockIdx.x;
+    if (warp < kSets) {
+        const int kind = warp == 1, first = warp == 2, begin = kind * u.parts, end = begin + u.parts, c = begin + blockIdx.x;
         // The first rounds' loads are in flight together, 32 parts back and ahead.
         const ChunkDesc none = {-1, 0, 0, 0};
         auto at = [&](int p, int last) {
@@ -127,6 +129,7 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
             from[warp] = kChunkMaxParts - before;
             count[warp] = d.b >= 0 ? before + after : 0;
             share[warp] = before;
+            shares[warp] = kind ? 1 : before + after;
             desc[warp] = d;
         }
     }
@@ -144,12 +147,11 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
     }
     bool bad = false;
 #pragma unroll 1
-    for (int set = 0; set < 4; ++set) {
+    for (int set = 0; set < kSets; ++set) {
         const ChunkDesc& d = desc[set];
-        const int n = count[set], rows = n ? d.nt() * u.k : 0;
+        const int n = count[set], rows = n ? d.nt() * u.k : 0, every = shares[set];
         const int* recs = list[set] + from[set];
-#pragma unroll 1
-        for (int r0 = (share[set] + n * warp) * kRows; r0 < rows; r0 += n * kCombineWarps * kRows) {
+        for (int r0 = (share[set] + every * warp) * kRows; r0 < rows; r0 += every * kCombineWarps * kRows) {
             // kRows rows and two parts at once, all their loads in flight together (with
             // the maxima in a pass of their own, and a row's loads after another's, 45 us
             // for 38 MB of records); lane holds elements kPer * lane ..  The running
@@ -167,7 +169,6 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) acc[i][e] = 0.f;
             }
-#pragma unroll 1
             for (int p = 0; p < n; p += 2) {
                 float lse[2][kRows], v[2][kRows][kPer];
 #pragma unroll
@@ -211,13 +212,13 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
         }
     }
     if (!__syncthreads_or(bad)) return;
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < kSets; ++x) {
         if (!count[x]) continue;
         const ChunkDesc d = desc[x];
         const ChunkSeq s = chunk_seq(u, d.b);
         ChunkItem it;
         chunk_item(u, s, d.b, d.q(), (d.t0 - s.t0) / u.WU, it);
-        unit_again<T, D>(u, it, share[x], count[x], warp, Q, Kp, Vp, scale_log2, O);
+        unit_again<T, D>(u, it, share[x], shares[x], warp, Q, Kp, Vp, scale_log2, O);
     }
 }
 
