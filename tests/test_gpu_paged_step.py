@@ -377,6 +377,50 @@ def test_two_calls_at_once():
         st.check()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_widest_table(dtype):
+    """page_size * max_blocks = 2^30, the largest allowed: the scale of the split's costs and the grid follow it."""
+    st = Step(U.gqe(), new=[1, 60, 0], ctx=[900, 70000, 5], h=4, gr=1, d=32, k=2, ps=65536, dtype=dtype, seed=14)
+    st.bt = torch.full((3, 1 << 14), -1, **INT)
+    for b, pages in enumerate(st.table):
+        st.bt[b, :len(pages)] = ints(pages)
+    st.run()
+    assert st.status() == 0
+    st.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_idle_requests(dtype):
+    """16384 requests of which few have work, the last among them."""
+    new = [0] * 16384
+    for b in (3, 700, 701, 9000, 16383):
+        new[b] = 1 + b % 40
+    st = Step(U.gqe(), new=new, ctx=[50 if a else 0 for a in new], h=4, gr=2, d=64, k=1, ps=8, dtype=dtype, pad=3, seed=15)
+    st.run()
+    assert st.status() == 0
+    st.check()
+
+
+@pytest.mark.parametrize("dtype,window", [(BF, 0), (BF, 300), (F32, 300)])
+def test_long_prompt_at_once_and_in_parts(dtype, window):
+    """20000 tokens of one request in one call, and the same in two."""
+    kw = dict(h=2, gr=1, d=32, k=1, ps=64, dtype=dtype, window=window, sinks=2, seed=16)
+    st = Step(U.gqe(), new=[20000], ctx=[0], **kw)
+    st.run()
+    whole, lengths, parts = st.O.clone(), st.lengths, torch.empty_like(st.O)
+    for a, b in ((0, 7001), (7001, 20000)):
+        part = Step(U.gqe(), new=[b - a], ctx=[a], **kw)
+        part.K, part.V, part.bt = st.K, st.V, st.bt
+        part.Q, part.idx, part.gate = (x[a:b].contiguous() for x in (st.Q, st.idx, st.gate))
+        part.run()
+        assert part.status() == 0
+        parts[a:b] = part.O
+    assert st.status() == 0 and lengths == [20000]
+    # |V| <= 6 here: each side rounds weights and result to half a step, fp32 its sums over at most 20000 keys
+    bound = 2 * (2 * 2.0 ** -8 * 6 if dtype == BF else 20000 * 2.0 ** -23 * 6)
+    assert (whole.float() - parts.float()).abs().max().item() <= bound
+
+
 def test_bad_requests_are_reported_and_skipped():
     g = U.gqe()
     for what in ("short", "long", "rows", "backwards"):
