@@ -304,9 +304,9 @@ def _device(fn, t):
     return dev
 
 
-def _dense(fn, dev, dtype, n, *tensors):
-    """Refuse a tensor that is not n dense elements of dtype on device dev."""
-    for t in tensors:
+def _dense(fn, dev, dtype, *tensors):
+    """Refuse a tensor that is not dense, of dtype on device dev; tensors: (tensor, its elements)."""
+    for t, n in tensors:
         if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
             raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
 
@@ -319,13 +319,9 @@ def gqe_page_plan(page_size, lengths, new_lens, free_pages, free_count, block_ta
     n, rows, pages, blocks, nbytes = (lengths.numel(), slots.numel(), free_pages.numel(), block_table.shape[-1],
                                       workspace.numel())
     dev = _device(fn, lengths)
-    _dense(fn, dev, i32, n, lengths, new_lens, lengths_out)
-    _dense(fn, dev, i32, 1, free_count, free_count_out)
-    _dense(fn, dev, i32, n * blocks, block_table)
-    _dense(fn, dev, i32, n + 1, cu_new)
-    _dense(fn, dev, i32, rows, slots)
-    _dense(fn, dev, i32, pages, free_pages)
-    _dense(fn, dev, torch.uint8, nbytes, workspace)
+    _dense(fn, dev, i32, (lengths, n), (new_lens, n), (lengths_out, n), (free_count, 1), (free_count_out, 1),
+           (block_table, n * blocks), (cu_new, n + 1), (slots, rows), (free_pages, pages))
+    _dense(fn, dev, torch.uint8, (workspace, nbytes))
     _check(fn, _lib.gqe_page_plan(
         n, rows, int(page_size), pages, blocks, lengths.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
         free_count.data_ptr(), block_table.data_ptr(), lengths_out.data_ptr(), free_count_out.data_ptr(),
@@ -337,7 +333,8 @@ def _pages(fn, dev, shape, dtype, K_pages, V_pages):
     dims = K_pages.shape
     if len(dims) != 4 or dims[2] != shape.g or dims[3] != shape.d_h or V_pages.shape != dims:
         raise GQEError(fn, GQE_ERR_INVALID_ARGUMENT)
-    _dense(fn, dev, dtype, K_pages.numel(), K_pages, V_pages)
+    n = K_pages.numel()
+    _dense(fn, dev, dtype, (K_pages, n), (V_pages, n))
     return dims[0], dims[1]
 
 
@@ -347,8 +344,8 @@ def gqe_kv_append(shape, K_new, V_new, slots, K_pages, V_pages, workspace, strea
     fn, dt, g, d = "gqe_kv_append", torch.bfloat16 if shape.dtype == GQE_BF16 else torch.float32, shape.g, shape.d_h
     rows, nbytes = shape.B * shape.T, workspace.numel()
     dev = _device(fn, slots)
-    _dense(fn, dev, torch.int32, rows, slots)
-    _dense(fn, dev, torch.uint8, nbytes, workspace)
+    _dense(fn, dev, torch.int32, (slots, rows))
+    _dense(fn, dev, torch.uint8, (workspace, nbytes))
     pages, page_size = _pages(fn, dev, shape, dt, K_pages, V_pages)
     strides = []
     for t in (K_new, V_new):
@@ -375,14 +372,11 @@ def gqe_attn_chunk_paged(shape, Q, K_pages, V_pages, block_table, cu_new, length
     fn, dt, T = "gqe_attn_chunk_paged", torch.bfloat16 if shape.dtype == GQE_BF16 else torch.float32, shape.T
     n, blocks, nbytes, i32 = lengths.numel(), block_table.shape[-1], workspace.numel(), torch.int32
     dev = _device(fn, Q)
-    _dense(fn, dev, dt, T * shape.h * shape.d_h, Q, O)
-    picks = T * shape.g * shape.k
-    _dense(fn, dev, i32, picks, idx)
-    _dense(fn, dev, torch.float32, picks, gate)
-    _dense(fn, dev, i32, n, lengths)
-    _dense(fn, dev, i32, n + 1, cu_new)
-    _dense(fn, dev, i32, n * blocks, block_table)
-    _dense(fn, dev, torch.uint8, nbytes, workspace)
+    rows, picks = T * shape.h * shape.d_h, T * shape.g * shape.k
+    _dense(fn, dev, dt, (Q, rows), (O, rows))
+    _dense(fn, dev, i32, (idx, picks), (lengths, n), (cu_new, n + 1), (block_table, n * blocks))
+    _dense(fn, dev, torch.float32, (gate, picks))
+    _dense(fn, dev, torch.uint8, (workspace, nbytes))
     pages, page_size = _pages(fn, dev, shape, dt, K_pages, V_pages)
     _check(fn, _lib.gqe_attn_chunk_paged(
         ctypes.byref(shape), Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), pages, page_size,

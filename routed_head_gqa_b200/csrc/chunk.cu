@@ -16,7 +16,9 @@ namespace {
 // One block per part: with blocks by part and row range, most of them with nothing
 // to do, 20 us went by on their starting and leaving.
 constexpr int kCombineWarps = 16;
-constexpr int kRows = 4;  // rows a warp merges at once
+// Rows a warp merges at once: with four, 3 decodes took 19.4 us for 18.3 and 128 windowed
+// ones 116 for 112 (registers, code); with one, prompts under a window 212 for 206.
+constexpr int kRows = 2;
 
 // The rows of a unit, of a share of its groups of kRows rows, whose result is not
 // finite from the formula, a warp each.
@@ -74,8 +76,8 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
                      float scale_log2, T* __restrict__ O) {
     constexpr int kRec = D + 4, kPer = D / 32;
     // The part's last units of many and few rows, and its first unit of many rows (a
-    // unit of few is a group or four of kRows: the block of its first part merges it
-    // alone): the unit, its records in order and this block's share of its groups.
+    // unit of few is a group for half of the warps at most: the block of its first part
+    // merges it alone): the unit, its records in order and this block's share of its groups.
     constexpr int kSets = 3;
     __shared__ int list[kSets][2 * kChunkMaxParts];  // the block's own part at kChunkMaxParts
     __shared__ int from[kSets], count[kSets], share[kSets], shares[kSets];
