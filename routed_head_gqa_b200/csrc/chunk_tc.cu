@@ -44,7 +44,7 @@
 //
 // Bounds and figures (d_h = 128, 32 heads in 8 groups, k = 2).  Decodes: HBM; 64 of
 // 1000 to 16000 keys, 64-row pages, 2.5 GB, 383 us or 6.55 TB/s, the rate of a plain
-// copy; 128 under a window of 1024, nine steps each, 115 us or 4.7 TB/s (a unit's end
+// copy; 128 under a window of 1024, nine steps each, 112 us or 4.8 TB/s (a unit's end
 // costs its groups about 2.5 us, under which the stages fill and then wait).  Prompts:
 // the exponentials and the S -> P -> O chain of a step, 3200 clocks of which the
 // products take 2048, and 12000 a unit (its first S and its epilogue overlap no
