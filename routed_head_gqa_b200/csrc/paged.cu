@@ -219,9 +219,13 @@ kv_append_kernel(const AppendArgs a, int vecs, int lanes) {
 }  // namespace
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
+    // Opting in to more than 48 KB, of static and dynamic together: from well below that,
+    // and always to the most a call can need, as the setting outlasts the call and another
+    // thread's, were it smaller, would refuse this one's launch.
+    constexpr size_t kMost = 3 * (size_t)(kPlanMaxSeqs + 1) * sizeof(int32_t);
     const size_t smem = 3 * (size_t)(a.n_seqs + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
-        cudaError_t err = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 32 * 1024) {
+        cudaError_t err = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (err != cudaSuccess) return err;
     }
     // one row (or request) per thread, up to a block per SM: a block's scan costs
