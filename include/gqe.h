@@ -511,7 +511,13 @@ gqe_status gqe_aux_loss(const gqe_shape* s, const float* logits, const int32_t* 
  * stack that would exceed num_pages.  Then cu_new is all 0, slots all -1,
  * lengths_out and free_count_out repeat the inputs, and free_pages and
  * block_table stay as they were.  An entry of free_pages or block_table outside
- * [0, num_pages) is reported as GQE_ERR_INVALID_ARGUMENT and its rows get slot -1.
+ * [0, num_pages) that the step reads is reported as GQE_ERR_INVALID_ARGUMENT and
+ * its rows get slot -1; the rest of the plan is made as if it were a page, which
+ * it stays in the table or on the stack.
+ * A page belongs to one request at a time, from the step that takes it until the
+ * request ends: all entries of an ended request up to its last row go back,
+ * those of pages that a window has left as well, and no check finds a page that
+ * is given back twice.
  * 1 <= n_seqs <= 16384; more return GQE_ERR_UNSUPPORTED.
  */
 gqe_status gqe_page_plan(int n_seqs, int rows, int page_size, int num_pages, int max_blocks, const int32_t* lengths,
@@ -568,8 +574,9 @@ gqe_status gqe_kv_append(const gqe_shape* s, const void* K_new, int64_t k_stride
  *   workspace        at least gqe_chunk_workspace_bytes(s) bytes; calls that share
  *                    it are ordered on one stream (graphs that may run at the same
  *                    time need one each)
- * Only pages that hold a visible key are read: block-table entries of pages
- * that the window has left may be stale.  Infinities and NaN in keys or values
+ * Only pages that hold a visible key are read: to this call, block-table entries
+ * of pages that the window has left may be stale (gqe_page_plan still gives them
+ * back when the request ends).  Infinities and NaN in keys or values
  * that a row does not see, and rows past a cache's length, do not reach it.
  * The result is the same in every run (no atomics on values).
  * Implemented cases: bf16 or fp32, d_h in {32, 64, 128}, T * h < 2^31 - 1.

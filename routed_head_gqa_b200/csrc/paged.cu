@@ -162,8 +162,9 @@ page_plan_kernel(const PlanArgs a) {
         a.block_table[(int64_t)b * a.max_blocks + blocks_of(b) + (i - need_at[b])] = page;
     }
     for (int j = gtid; j < (int)total.back; j += gsize) {
-        const int b = find_owner(back_at, n, j);
-        a.free_pages[count + j] = a.block_table[(int64_t)b * a.max_blocks + (j - back_at[b])];
+        const int b = find_owner(back_at, n, j), page = a.block_table[(int64_t)b * a.max_blocks + (j - back_at[b])];
+        check(page);  // here, or a later step would blame the request that takes it
+        a.free_pages[count + j] = page;
     }
     for (int b = gtid; b <= n; b += gsize) {
         a.cu_new[b] = rows_at[b];

@@ -1,5 +1,6 @@
 """Edges of the paged serving step on the GPU: the page plan's shared memory by
-the number of requests, in a fresh process and from two threads."""
+the number of requests, in a fresh process and from several threads; bad pages
+of ended requests."""
 import subprocess
 import sys
 import threading
@@ -8,7 +9,7 @@ import pytest
 import torch
 
 from tests import gpu_util as U
-from tests.test_gpu_paged_step import ints
+from tests.test_gpu_paged_step import ints, run_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +65,21 @@ def test_plans_of_several_sizes_from_several_threads():
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+@pytest.mark.parametrize("page", [-1, 12, 2 ** 31 - 1])
+def test_plan_reports_bad_pages_of_an_ended_request(page):
+    """An ended request whose block table holds an entry outside the pool: reported in the step that pushes it, not in
+    the later one of another request that takes it.  Everything else of the plan is as if the entry were a page."""
+    g = U.gqe()
+    lengths, new, free = [5, 3, 4], [1, -1, 1], [9, 8]
+    table = [[0, 1, -1], [page, -1, -1], [3, -1, -1]]
+    fp, bt, lo, fo, cu, slots, status = run_plan(g, 4, 12, 2, lengths, [1, -1, 0], free, table)
+    assert status == g.GQE_ERR_INVALID_ARGUMENT
+    assert lo == [6, 0, 4] and fo == 3 and fp[:3] == [9, 8, page] and bt == table and slots == [5, -1]
+    # taken in the same step as well: request 2 starts its second page
+    fp, bt, lo, fo, cu, slots, status = run_plan(g, 4, 12, 2, lengths, new, free, table)
+    assert status == g.GQE_ERR_INVALID_ARGUMENT and lo == [6, 0, 5] and fo == 2 and slots == [5, -1]
+    # a block behind the request's last row is not pushed, and so not looked at
+    table[1] = [2, page, page]
+    assert run_plan(g, 4, 12, 2, lengths, new, free, table)[-1] == g.GQE_OK
