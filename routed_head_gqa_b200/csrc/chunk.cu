@@ -82,7 +82,6 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
     __shared__ int list[kSets][2 * kChunkMaxParts];  // the block's own part at kChunkMaxParts
     __shared__ int from[kSets], count[kSets], share[kSets], shares[kSets];
     __shared__ ChunkDesc desc[kSets];
-    __shared__ ChunkSplit split;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -138,13 +137,10 @@ chunk_combine_kernel(const __grid_constant__ ChunkGeom u, const T* __restrict__ 
     if (__syncthreads_or(odd)) {
         for (int kind = 0; kind < 2; ++kind) {
             if (!u.odd[kind * u.parts + blockIdx.x]) continue;  // the same for the whole block
-            // the flags are by CTA
-            chunk_split<32 * kCombineWarps>(u, split, blockIdx.x);
-            ChunkWalk walk(u, split, kind, blockIdx.x);
+            ChunkWalk walk(u, kind, blockIdx.x);  // the flags are by CTA
             ChunkItem it;
             while (walk.next(u, it, false))
                 if (it.rec < 0) unit_again<T, D>(u, it, 0, 1, warp, Q, Kp, Vp, scale_log2, O);
-            __syncthreads();  // split may be overwritten
         }
     }
     bool bad = false;
@@ -259,6 +255,7 @@ int few_cap(const gqe_shape* s, const ChunkTiling& t) {
 }
 
 size_t desc_bytes(int parts) { return a256(4 * (size_t)parts * sizeof(ChunkDesc)); }
+size_t place_bytes(int parts) { return a256(4 * (size_t)parts * sizeof(ChunkPlace)); }
 size_t odd_bytes(int parts) { return a256(2 * (size_t)parts * sizeof(int32_t)); }
 
 ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
@@ -302,8 +299,10 @@ ChunkGeom make_geom(const ChunkArgs& a, const ChunkTiling& t, int parts) {
     u.gate = a.gate;
     u.status = a.status;
     u.desc = static_cast<ChunkDesc*>(a.scratch);
-    u.odd = reinterpret_cast<int32_t*>(static_cast<char*>(a.scratch) + desc_bytes(parts));
-    u.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) + desc_bytes(parts) + odd_bytes(parts));
+    char* at = static_cast<char*>(a.scratch) + desc_bytes(parts);
+    u.place = reinterpret_cast<ChunkPlace*>(at);
+    u.odd = reinterpret_cast<int32_t*>(at += place_bytes(parts));
+    u.part = reinterpret_cast<float*>(at += odd_bytes(parts));
     return u;
 }
 
@@ -334,7 +333,7 @@ cudaError_t launch_combine(const ChunkGeom& u, const ChunkArgs& a) {
 size_t chunk_scratch_bytes(const gqe_shape* s) {
     const ChunkTiling t = tiling(s);
     const size_t parts = (size_t)max_parts(t), rows = 2 * parts * (row_cap(s, t) + few_cap(s, t));
-    return desc_bytes((int)parts) + odd_bytes((int)parts) + a256(rows * (size_t)(s->d_h + 4) * sizeof(float));
+    return desc_bytes((int)parts) + place_bytes((int)parts) + odd_bytes((int)parts) + a256(rows * (size_t)(s->d_h + 4) * sizeof(float));
 }
 
 cudaError_t launch_chunk(const ChunkArgs& a) {

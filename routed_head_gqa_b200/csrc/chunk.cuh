@@ -43,6 +43,11 @@ struct __align__(16) ChunkDesc {
     }
 };
 
+// A place in the order of units: request, group, unit within both, step.
+struct __align__(16) ChunkPlace {
+    int b, q, i, s;
+};
+
 struct ChunkGeom {
     int T, n_seqs, h, g, k, hpg;
     uint32_t inv_k;   // row / k == row * inv_k >> 16 for a unit's rows
@@ -65,6 +70,7 @@ struct ChunkGeom {
     const float* gate;
     void* status;
     ChunkDesc* desc;  // [2 kinds][parts][2]
+    ChunkPlace* place;  // [2 kinds][CTAs][2]: where the CTA's work starts, and the first place that is no longer its own
     int32_t* odd;     // [2 kinds][CTAs]: a result of the CTA's whole units is not finite
     float* part;      // [2 * parts * row_cap + 2 * parts * few_cap][D + 4]
 };
@@ -154,11 +160,6 @@ __device__ __forceinline__ void chunk_item(const ChunkGeom& u, const ChunkSeq& s
 __device__ __forceinline__ bool chunk_sees(const ChunkGeom& u, int p, int s) {
     return s <= p && (u.window == 0 || s > p - u.window || s < u.sinks);
 }
-
-// A place in the order of units: request, group, unit within both, step.
-struct ChunkPlace {
-    int b, q, i, s;
-};
 
 // Where a fraction (0 or more, below 1) of request b's work ends (warp-collective,
 // the same in every lane).
@@ -287,6 +288,22 @@ struct ChunkWalk {
             if (e.b < u.n_seqs) at = chunk_place(u, e.seq, e.b, e.fraction);
             seq = e.seq;
         }
+    }
+    // The walk of a CTA of the tile kernel again, in the merge: from the places that it
+    // left.  Its own split of the step might place a border one step off, as the
+    // compiler is free to round the costs in another way in another kernel.
+    __device__ __forceinline__ ChunkWalk(const ChunkGeom& u, int kind, int cta) : kind(kind), part(chunk_part(u, kind, cta)) {
+        at = u.place[2 * (kind * u.parts + cta)];
+        to = u.place[2 * (kind * u.parts + cta) + 1];
+        base = at.b;
+        seq = {0, 0, 0};
+        if (at.b < u.n_seqs) seq = chunk_seq(u, at.b);
+        fetch(u);
+    }
+    // Leaves the places of a fresh walk for the merge (one thread).
+    __device__ __forceinline__ void leave(const ChunkGeom& u, int cta) const {
+        u.place[2 * (kind * u.parts + cta)] = at;
+        u.place[2 * (kind * u.parts + cta) + 1] = to;
     }
     __device__ __forceinline__ void fetch(const ChunkGeom& u) {
         const int b = base + (threadIdx.x & 31);

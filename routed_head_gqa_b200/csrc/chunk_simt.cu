@@ -402,6 +402,7 @@ chunk_simt_kernel(const __grid_constant__ ChunkGeom u, const float* __restrict__
     chunk_split<kThreads>(u, sh.split, blockIdx.x);
     if (!chunk_has(u, sh.split, 0)) return;
     ChunkWalk walk(u, sh.split, 0, blockIdx.x);
+    if (tid == 0) walk.leave(u, blockIdx.x);
     while (true) {
         if (tid < 32) {
             ChunkItem it;

@@ -752,6 +752,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         for (int phase = 0; phase < phases && ok; ++phase) {
             const bool few = (phase == 0) == few_first;
             ChunkWalk walk(u, sm.split, few, blockIdx.x);
+            if (lane == 0) walk.leave(u, blockIdx.x);
 #pragma unroll 1
             for (; !aborted(sm); ++ui) {
                 const int slot = ui % kItems;

@@ -1,6 +1,7 @@
 """Edges of the paged serving step on the GPU: the page plan's shared memory by
 the number of requests, in a fresh process and from several threads; bad pages
-of ended requests."""
+of ended requests; rows that are taken again, wherever the split of a step falls."""
+import random
 import subprocess
 import sys
 import threading
@@ -9,7 +10,8 @@ import pytest
 import torch
 
 from tests import gpu_util as U
-from tests.test_gpu_paged_step import ints, run_plan
+from tests import paged_ref as R
+from tests.test_gpu_paged_step import BF, F32, Step, ints, run_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +85,44 @@ def test_plan_reports_bad_pages_of_an_ended_request(page):
     # a block behind the request's last row is not pushed, and so not looked at
     table[1] = [2, page, page]
     assert run_plan(g, 4, 12, 2, lengths, new, free, table)[-1] == g.GQE_OK
+
+
+# ------------------------------------------------------------------ attention
+def group_rows(st, b, q, tokens):
+    """[T, h, d] mask of the selected heads of group q of request b's new tokens (a range)."""
+    hit = torch.zeros_like(st.O, dtype=torch.bool)
+    for i in tokens:
+        t = st.cu[b] + i
+        hit[t, st.idx[t, q].long()] = True
+    return hit
+
+
+def within(st, clean, sel):
+    """st.O is within the tolerance of the formula on clean's inputs where sel."""
+    O, mag, wob = R.attention(clean.Q, clean.K, clean.V, clean.table, clean.cu, clean.lengths, st.window, st.sinks, clean.idx, clean.gate)
+    n = st.cu[-1]
+    err, tol = (st.O[:n].double() - O[:n]).abs(), R.tolerance(O, mag, wob, st.dtype, max(st.lengths))[:n]
+    return bool((err <= tol)[sel[:n]].all())
+
+
+@pytest.mark.parametrize("kw", [dict(d=64), dict(gr=3, h=9, d=32), dict(dtype=F32, d=32, gr=3, h=9)], ids=["bf16", "bf16 3 groups", "f32 3 groups"])
+def test_rows_are_taken_again_wherever_the_split_falls(kw):
+    """In steps whose parts begin and end anywhere, the last new token of each chunk has values of NaN; the rows before
+    it, of whole units and of split ones, are as without them.  The merge has to find the units that the tile kernel
+    found."""
+    for seed in range(12):
+        r = random.Random(seed)
+        n = r.randint(3, 160)
+        new = [r.choice([1, r.randint(2, 30), r.randint(2, 150)]) for _ in range(n)]
+        step = dict(new=new, ctx=[r.randint(0, 700) for _ in range(n)], k=r.choice([1, 2, 3]), ps=r.choice([4, 16, 64]), window=r.choice([0, 0, 130]),
+                    sinks=3, seed=seed, **kw)
+        st, clean = Step(U.gqe(), **step), Step(U.gqe(), **step)
+        sees = torch.zeros_like(st.O, dtype=torch.bool)
+        for b, a in enumerate(new):
+            st.V.view(-1, *st.V.shape[2:])[st.rows_of(b)[-1]] = float("nan")
+            for q in range(st.idx.shape[1]):
+                sees |= group_rows(st, b, q, [a - 1])
+        st.run()
+        assert st.status() == 0
+        assert torch.equal(torch.isnan(st.O), sees), step
+        assert within(st, clean, ~sees), step
