@@ -112,9 +112,12 @@ __device__ __forceinline__ int chunk_units(const ChunkGeom& u, int n) { return (
 
 // Cost, in keys, of the first i units of a request and group in closed form: unit j
 // sees about first + j * WU keys, or the window's span if that is less.  fp32, as
-// they only place the boundaries and every CTA evaluates the same expressions on
-// the same numbers; the prefix sums over requests are in whole numbers, whose
-// intervals tile without gaps.
+// they only place the boundaries, but every evaluation has to give the same number
+// (a request's cost is summed by one and searched by another, and a boundary that
+// neither side owns would lose its work), so each product and sum is rounded by
+// itself: left to the compiler, copies of the code may contract them differently.
+// The prefix sums over requests are in whole numbers, whose intervals tile without
+// gaps.
 struct ChunkCost {
     float first, span, grow;  // units before `grow` still grow
     __device__ __forceinline__ ChunkCost(const ChunkGeom& u, const ChunkSeq& s)
@@ -128,11 +131,11 @@ struct ChunkCost {
     }
     __device__ __forceinline__ float operator()(const ChunkGeom& u, int units) const {
         const float i = (float)units, n = fminf(i, grow);
-        return n * (first + 0.5f * u.WU * (n - 1.f)) + (i - n) * span;
+        return __fadd_rn(__fmul_rn(n, __fmaf_rn(0.5f * u.WU, n - 1.f, first)), __fmul_rn(i - n, span));
     }
 };
 __device__ __forceinline__ uint32_t chunk_cost(const ChunkGeom& u, const ChunkSeq& s) {
-    return s.n > 0 ? max(__float2uint_rn(u.g * ChunkCost(u, s)(u, chunk_units(u, s.n)) * u.cost_scale), 1u) : 0;
+    return s.n > 0 ? max(__float2uint_rn(__fmul_rn(__fmul_rn((float)u.g, ChunkCost(u, s)(u, chunk_units(u, s.n))), u.cost_scale)), 1u) : 0;
 }
 
 __device__ __forceinline__ void chunk_item(const ChunkGeom& u, const ChunkSeq& s, int b, int q, int i, ChunkItem& it) {

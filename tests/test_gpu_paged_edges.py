@@ -126,3 +126,23 @@ def test_rows_are_taken_again_wherever_the_split_falls(kw):
         assert st.status() == 0
         assert torch.equal(torch.isnan(st.O), sees), step
         assert within(st, clean, ~sees), step
+
+
+def test_prompt_whose_cost_needs_more_than_24_bits():
+    """150000 tokens of one request, whose units see 45 million keys together: the fp32 costs that place the split are
+    rounded.  At once as in parts, beside decodes."""
+    kw = dict(h=2, gr=1, d=32, k=1, ps=64, seed=17)
+    n, cuts = 150000, (0, 40001, 90003, 150000)
+    st = Step(U.gqe(), new=[1, n, 1], ctx=[70, 0, 9], **kw)
+    st.run()
+    parts = torch.full_like(st.O, 7)
+    for a, b in zip(cuts, cuts[1:]):
+        part = Step(U.gqe(), new=[b - a], ctx=[a], **kw)
+        part.K, part.V, part.bt = st.K, st.V, st.bt[1:2].contiguous()
+        part.Q, part.idx, part.gate = (x[1 + a:1 + b].contiguous() for x in (st.Q, st.idx, st.gate))
+        part.run()
+        assert part.status() == 0
+        parts[1 + a:1 + b] = part.O
+    assert st.status() == 0
+    # as in the test of 20000 tokens: |V| <= 6, each side rounds the weights and the result to half a step
+    assert (st.O[1:1 + n].float() - parts[1:1 + n].float()).abs().max().item() <= 2 * 2 * 2.0 ** -8 * 6
