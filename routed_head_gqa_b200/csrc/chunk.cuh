@@ -71,7 +71,7 @@ struct ChunkGeom {
     void* status;
     ChunkDesc* desc;  // [2 kinds][parts][2]
     ChunkPlace* place;  // [2 kinds][CTAs][2]: where the CTA's work starts, and the first place that is no longer its own
-    int32_t* odd;     // [2 kinds][CTAs]: a result of the CTA's whole units is not finite
+    int32_t* odd;     // [2 kinds][CTAs]: some result of the CTA's units is not finite
     float* part;      // [2 * parts * row_cap + 2 * parts * few_cap][D + 4]
 };
 
@@ -292,17 +292,6 @@ struct ChunkWalk {
             seq = e.seq;
         }
     }
-    // The walk of a CTA of the tile kernel again, in the merge: from the places that it
-    // left.  Its own split of the step might place a border one step off, as the
-    // compiler is free to round the costs in another way in another kernel.
-    __device__ __forceinline__ ChunkWalk(const ChunkGeom& u, int kind, int cta) : kind(kind), part(chunk_part(u, kind, cta)) {
-        at = u.place[2 * (kind * u.parts + cta)];
-        to = u.place[2 * (kind * u.parts + cta) + 1];
-        base = at.b;
-        seq = {0, 0, 0};
-        if (at.b < u.n_seqs) seq = chunk_seq(u, at.b);
-        fetch(u);
-    }
     // Leaves the places of a fresh walk for the merge (one thread).
     __device__ __forceinline__ void leave(const ChunkGeom& u, int cta) const {
         u.place[2 * (kind * u.parts + cta)] = at;
@@ -317,8 +306,7 @@ struct ChunkWalk {
             L = u.lengths[b];
         }
     }
-    // describe: write the descriptors of split units
-    __device__ __forceinline__ bool next(const ChunkGeom& u, ChunkItem& it, bool describe = true) {
+    __device__ __forceinline__ bool next(const ChunkGeom& u, ChunkItem& it) {
         if (at.b >= u.n_seqs) return false;
         if (at.i >= chunk_units(u, seq.n)) {
             at.i = 0;
@@ -354,7 +342,7 @@ struct ChunkWalk {
         if (it.s0 > 0 || it.s1 < it.steps) {
             const int slot = it.s0 > 0 ? 2 * part : 2 * part + 1;
             it.rec = kind ? 2 * u.parts * u.row_cap + slot * u.few_cap : slot * u.row_cap;
-            if ((threadIdx.x & 31) == 0 && describe) u.desc[kind * 2 * u.parts + slot] = {it.b, it.t0, it.q << 16 | it.nt, it.rec};
+            if ((threadIdx.x & 31) == 0) u.desc[kind * 2 * u.parts + slot] = {it.b, it.t0, it.q << 16 | it.nt, it.rec};
         }
         ++at.i;
         at.s = 0;
@@ -395,65 +383,6 @@ __device__ __forceinline__ int chunk_head(const ChunkGeom& u, int token, int q, 
         return -1;
     }
     return j;
-}
-
-// One row of a unit by the formula alone, key by key over the keys the row sees
-// (warp-collective; lane holds elements e * 32 + lane).  The tile kernels multiply
-// a masked key's weight 0 with its V row, so an infinity or NaN there reaches rows
-// that do not see the key; a row whose result is not finite is therefore taken
-// again here (by the merge kernel: in the tile kernels the code alone would cost
-// their loops registers), where a key that the row does not see is not read.
-template <typename T, int D>
-__device__ __forceinline__ void chunk_row(const ChunkGeom& u, const ChunkItem& it, int p, const T* q_row, const T* Kp,
-                                          const T* Vp, float scale_log2, float (&acc)[D / 32], float& m, float& l) {
-    const int lane = threadIdx.x & 31;
-    float qv[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-        qv[e] = Elem<T>::to_f(q_row[e * 32 + lane]);
-        acc[e] = 0.f;
-    }
-    m = -INFINITY;
-    l = 0.f;
-#pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-        const int k0 = part ? it.head + it.skip : 0, k1 = part ? p + 1 : it.head;
-        for (int s = k0; s < k1; s += 4) {  // four keys' loads in flight
-            float x[4], v[4][D / 32];
-            bool on[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                on[j] = s + j < k1 && chunk_sees(u, p, s + j);
-                x[j] = 0.f;
-                if (on[j]) {
-                    const int64_t at = (chunk_cache_row(u, it.b, s + j) * u.g + it.q) * D;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) {
-                        x[j] = fmaf(qv[e], Elem<T>::to_f(Kp[at + e * 32 + lane]), x[j]);
-                        v[j][e] = Elem<T>::to_f(Vp[at + e * 32 + lane]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) x[j] += __shfl_xor_sync(0xffffffffu, x[j], d);
-                x[j] *= scale_log2;
-                if (!on[j] || x[j] == -INFINITY) continue;  // -inf: weight 0 beside any other key
-                const float mx = fmaxf(m, x[j]);
-                const float corr = m == -INFINITY ? 0.f : fast_exp2(m - mx), w = fast_exp2(x[j] - mx);
-                m = mx;
-                l = l * corr + w;
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) acc[e] = acc[e] * corr + w * v[j][e];
-            }
-            if (l != l) {  // a score was NaN: so is the whole row
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) acc[e] = l;
-                return;
-            }
-        }
-    }
 }
 
 // Arguments of a call (host).

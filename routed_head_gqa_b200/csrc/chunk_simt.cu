@@ -373,12 +373,12 @@ __device__ __forceinline__ void run_few(const ChunkGeom& u, const ChunkItem& it,
             if (i == r) mr = m[i];
         const bool none = mr == -INFINITY && sum == 0.f;
         const int token = it.t0 + r / u.k;
+        if (!(o * 0.f + sum * 0.f == 0.f)) u.odd[blockIdx.x] = 1;
         if (partial) {
             float* rec = u.part + (int64_t)(it.rec + r) * (D + 4);
             rec[c] = none ? 0.f : o / sum;
             if (c == 0) rec[D] = none ? -INFINITY : mr + log2f(sum);
         } else {
-            if (!(o * 0.f + sum * 0.f == 0.f)) u.odd[blockIdx.x] = 1;
             O[((int64_t)token * u.h + j) * D + c] =
                 o * (u.gate[((int64_t)token * u.g + it.q) * u.k + r % u.k] / sum);
         }

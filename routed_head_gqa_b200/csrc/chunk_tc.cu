@@ -499,7 +499,7 @@ __device__ __forceinline__ bool few_item(const ChunkGeom& u, const Params& p, Sm
             p.O[(int64_t)out * d + col] = __float2bfloat16_rn(v * (gm / l[r]));
         }
     }
-    if (!(check == 0.f) && !partial) u.odd[u.parts + blockIdx.x] = 1;
+    if (!(check == 0.f)) u.odd[u.parts + blockIdx.x] = 1;
     return true;
 }
 
@@ -1179,7 +1179,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 32; ++e) check[e & 3] = fmaf(__uint_as_float(o[cb][e]), 0.f, check[e & 3]);
             if (out_row >= 0) {
-                if (!partial && !((check[0] + check[1]) + (check[2] + check[3]) == 0.f)) u.odd[blockIdx.x] = 1;
+                if (!((check[0] + check[1]) + (check[2] + check[3]) == 0.f)) u.odd[blockIdx.x] = 1;
                 if (partial) u.part[(int64_t)(rec_row + lane) * (d + 4) + d] = none ? -INFINITY : m + log2f(l);
             }
             uint4* stage = sm.stage(t, wq);

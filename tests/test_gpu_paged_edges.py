@@ -1,6 +1,6 @@
 """Edges of the paged serving step on the GPU: the page plan's shared memory by
 the number of requests, in a fresh process and from several threads; bad pages
-of ended requests; rows that are taken again, wherever the split of a step falls."""
+of ended requests; infinities and NaN in rows that some tokens see and others do not."""
 import random
 import subprocess
 import sys
@@ -146,3 +146,85 @@ def test_prompt_whose_cost_needs_more_than_24_bits():
     assert st.status() == 0
     # as in the test of 20000 tokens: |V| <= 6, each side rounds the weights and the result to half a step
     assert (st.O[1:1 + n].float() - parts[1:1 + n].float()).abs().max().item() <= 2 * 2 * 2.0 ** -8 * 6
+
+
+SHAPES = {"bf16": dict(ps=16), "bf16 d64 ps4": dict(d=64, ps=4), "bf16 window": dict(window=150, sinks=6), "f32": dict(dtype=F32, d=64), "f32 window": dict(dtype=F32, d=32, window=70)}
+
+
+@pytest.mark.parametrize("kw", SHAPES.values(), ids=SHAPES)
+def test_what_rows_see_spoils_its_own_elements_only(kw):
+    """A NaN in one element of a value that all rows of a request see, and an infinity in another: those elements of the
+    group's selected heads are not finite, every other one is the same bit for bit.  Nothing is taken again."""
+    kw = dict(new=[60, 1, 300, 1, 7], ctx=[400, 700, 900, 6000, 33], seed=21, **kw)
+    st, clean = Step(U.gqe(), **kw), Step(U.gqe(), **kw)
+    hit = torch.zeros_like(st.O, dtype=torch.bool)
+    for b in range(5):
+        row = st.rows_of(b)[kw["ctx"][b] - 3 if not st.window else st.lengths[b] - 1]
+        if st.window and kw["new"][b] > 1:
+            continue
+        st.V.view(-1, *st.V.shape[2:])[row, 1, 3] = float("nan")
+        st.V.view(-1, *st.V.shape[2:])[row, 1, 17] = float("inf")
+        hit |= group_rows(st, b, 1, range(kw["new"][b]))
+    hit[:, :, [i for i in range(hit.shape[2]) if i not in (3, 17)]] = False
+    st.run()
+    clean.run()
+    assert st.status() == 0 and hit.any()
+    assert torch.equal(~torch.isfinite(st.O), hit)
+    assert torch.equal(st.O[~hit], clean.O[~hit])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,d,ctx", [(BF, 128, 900), (BF, 32, 6000), (F32, 64, 900)], ids=["bf16", "bf16 d32", "f32"])
+def test_values_at_both_edges_of_a_window(dtype, d, ctx, value):
+    """Rows near a value that is not finite, in cached keys that the window is leaving and in new ones: each row has it if
+    it sees it.  Elements of one value are mixed: rows that see the one do not see the other."""
+    kw = dict(new=[300, 5, 1], ctx=[ctx, 90, 400], window=150, sinks=4, d=d, dtype=dtype, k=3, h=10, seed=22)
+    st, clean = Step(U.gqe(), **kw), Step(U.gqe(), **kw)
+    hit = torch.zeros_like(st.O, dtype=torch.bool)
+    planted = [(0, ctx - 100, 0, 5), (0, ctx + 37, 0, 5), (0, ctx + 210, 0, 9), (0, ctx + 211, 1, 9), (0, 3, 1, 30), (1, 92, 0, 7), (1, 2, 1, 8)]
+    for b, key, q, e in planted:
+        st.V.view(-1, *st.V.shape[2:])[st.rows_of(b)[key], q, e] = value
+        first = st.lengths[b] - kw["new"][b]
+        seen = [i for i in range(kw["new"][b]) if key <= first + i and (key > first + i - 150 or key < 4)]
+        rows = group_rows(st, b, q, seen)
+        rows[:, :, [x for x in range(d) if x != e]] = False
+        hit |= rows
+    st.run()
+    assert st.status() == 0
+    assert torch.equal(~torch.isfinite(st.O), hit)
+    assert within(st, clean, ~hit)
+    first = st.O.clone()
+    st.run()
+    assert torch.equal(torch.nan_to_num(first.float(), nan=77.0), torch.nan_to_num(st.O.float(), nan=77.0)), "two runs differ"
+
+
+@pytest.mark.parametrize("which", ["every value of one old key", "one element", "half of the new rows", "the last new row"])
+@pytest.mark.parametrize("new", [[2048], [1] * 64], ids=["prompt", "decodes"])
+def test_a_request_of_nan_does_not_hold_up_the_step(new, which):
+    """A step with NaN takes the time of the step without, within a factor (2 to 13 for the prompt, 1 for the decodes).
+    When each row that is not finite took its whole cache again, the prompt took 570 to 790 times as long and the
+    decodes 20 to 80."""
+    st = Step(U.gqe(), new=new, ctx=[12000 if len(new) == 1 else 8000] * len(new), h=32, gr=8, k=2, ps=64, seed=23)
+
+    def timed():
+        st.run()
+        best = 1e9
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            st.run()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    clean = timed()
+    rows, K, V = st.rows_of(0), st.K.view(-1, 8, 128), st.V.view(-1, 8, 128)
+    if which == "one element":
+        V[rows[5], :, 3] = float("nan")
+    elif which == "half of the new rows":
+        K[rows[-((new[0] + 1) // 2):]] = V[rows[-((new[0] + 1) // 2):]] = float("nan")
+    else:
+        V[rows[5 if which.startswith("every") else -1]] = float("nan")
+    assert timed() <= 40 * clean
+    assert st.status() == 0
