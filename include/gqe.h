@@ -560,9 +560,10 @@ gqe_status gqe_kv_append(const gqe_shape* s, const void* K_new, int64_t k_stride
  *
  *   s                B must be 1, T = the rows of Q, idx, gate and O
  *   Q, O [T, h, d_h], idx, gate [T, g, k] as for gqe_attn_prefill; a head outside
- *                    its group is reported in the status word and its row skipped
- *                    (a token's heads must differ, as the router picks them; O is
- *                    other memory than Q)
+ *                    its group is reported in the status word and its row skipped:
+ *                    the token's other heads are as without it, and 0 where none of
+ *                    its selections names them (a token's heads must differ, as the
+ *                    router picks them; O is other memory than Q)
  *   K_pages, V_pages, num_pages, page_size, block_table, max_blocks
  *                    as for gqe_attn_decode_paged; page_size * max_blocks <= 2^30
  *   cu_new [n_seqs + 1], lengths [n_seqs]   device int32: as gqe_page_plan writes

@@ -914,7 +914,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
         // the unit's first step: a bulk copy of a row of zeros each, the k threads of
         // a token taking its slots in turn.
         auto zero_fill = [&](const ChunkItem& it, int toks) {
-            if (it.s0 != 0 || u.k == u.hpg || r >= toks * u.k) return;
+            if (it.s0 != 0 || r >= toks * u.k) return;  // k of hpg heads or all, of which some may be none
             const int32_t* rows = sm.row[ui % kItems][t] + (r - sel);
             const int first = (it.t0 + off) * u.h + it.q * u.hpg;
             bf16* o = p.O + (int64_t)first * d;

@@ -1,6 +1,7 @@
 """Edges of the paged serving step on the GPU: the page plan's shared memory by
 the number of requests, in a fresh process and from several threads; bad pages
-of ended requests; infinities and NaN in rows that some tokens see and others do not."""
+of ended requests; infinities and NaN in rows that some tokens see and others do not; selections
+of heads outside their group."""
 import random
 import subprocess
 import sys
@@ -228,3 +229,42 @@ def test_a_request_of_nan_does_not_hold_up_the_step(new, which):
         V[rows[5 if which.startswith("every") else -1]] = float("nan")
     assert timed() <= 40 * clean
     assert st.status() == 0
+
+
+HEADS = {"decodes": dict(new=[1] * 9, ctx=[400, 0, 127, 700, 63, 64, 5, 1290, 90]), "split decode": dict(new=[1], ctx=[30000], ps=64),
+         "chunks": dict(new=[40, 3, 300, 1, 129], ctx=[60, 50, 10, 800, 0], pad=2), "split chunks": dict(new=[200, 256], ctx=[9000, 3000], ps=64),
+         "decodes k8": dict(new=[1, 2, 1], ctx=[500, 90, 3], h=16, k=8), "d32 ps4": dict(new=[20, 1, 130], ctx=[0, 90, 200], d=32, ps=4, k=3, h=10),
+         "window": dict(new=[200, 1], ctx=[700, 300], window=90, sinks=4, d=64)}
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name", HEADS)
+def test_bad_heads_are_skipped(name, dtype):
+    """Selections outside their group, in first, last and middle tokens and slots: reported; every other selection of the
+    same token and all other tokens as they are, and every slot that no good selection names is 0."""
+    g = U.gqe()
+    st = Step(g, seed=31, **{**HEADS[name], "dtype": dtype})
+    clean = Step(g, seed=31, **{**HEADS[name], "dtype": dtype})
+    T, gr, k = st.cu[-1], st.idx.shape[1], st.idx.shape[2]
+    h = st.O.shape[1]
+    r = random.Random(name)
+    bad = [(0, 0, 0, -1), (T - 1, gr - 1, k - 1, h)]
+    bad += [(r.randrange(T), r.randrange(gr), r.randrange(k), None) for _ in range(min(T // 8, 40))]
+    for t, q, slot, j in bad:
+        others = [x for x in (2 ** 31 - 1, -2 ** 31, (q + 1) * (h // gr), q * (h // gr) - 1) if j is None]
+        st.idx[t, q, slot] = r.choice(others) if others else j
+    st.run()
+    assert st.status() == g.GQE_ERR_INVALID_ARGUMENT
+    first = torch.arange(gr, device="cuda")[:, None] * (h // gr)
+    good = (st.idx >= first) & (st.idx < first + h // gr)
+    named = torch.zeros(st.O.shape[0], h, dtype=torch.bool, device="cuda")
+    for slot in range(k):
+        for q in range(gr):
+            t = good[:T, q, slot].nonzero().flatten()
+            named[t, st.idx[t, q, slot].long()] = True
+    assert (st.O[:T][~named[:T]] == 0).all()
+    assert (st.O[T:] == 7).all()
+    assert within(st, clean, named[:, :, None].expand_as(st.O))
+    # a bad selection changes nothing else, bit for bit
+    clean.run()
+    assert torch.equal(st.O[named], clean.O[named])
