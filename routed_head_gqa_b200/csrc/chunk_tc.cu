@@ -43,12 +43,14 @@
 // memory as the second operand.
 //
 // Bounds and figures (d_h = 128, 32 heads in 8 groups, k = 2).  Decodes: HBM; 64 of
-// 1000 to 16000 keys, 64-row pages, 2.5 GB, 383 us or 6.55 TB/s, the rate of a plain
-// copy; 128 under a window of 1024, nine steps each, 112 us or 4.8 TB/s (a unit's end
+// 1000 to 16000 keys, 64-row pages, 2.5 GB, 389 us or 6.46 TB/s (a plain copy: 6.55);
+// 128 under a window of 1024, nine steps each, 112 us or 4.8 TB/s (a unit's end
 // costs its groups about 2.5 us, under which the stages fill and then wait).  Prompts:
 // the exponentials and the S -> P -> O chain of a step, 3200 clocks of which the
 // products take 2048, and 12000 a unit (its first S and its epilogue overlap no
-// products): two chunks of 4096 tokens behind 12000 to 28000 keys run at 990 TFLOP/s.
+// products): two chunks of 4096 tokens behind 12000 to 28000 keys, 1.64 to 1.66 ms or
+// 930 TFLOP/s at the power cap.  Narrow heads move half or a quarter of the bytes in the
+// same chain of waits: the 64 decodes with d_h = 64, 281 us or 4.0 TB/s, d_h = 32, 241 us.
 //
 // Rounding: P is rounded to bf16 for the second product (half a step, 2^-8 of
 // each weight, the same size as the output's own rounding); the row sums take
@@ -1252,6 +1254,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant_
 
 }  // namespace
 
+// A unit's fixed cost is set to five steps of many rows and one of few, and the smallest
+// part to two steps.  With 2, 4 or 8 steps for many rows, a step of 28 decodes and 4 chunks
+// takes 139.7, 139.2 and 140.2 us for 139.4 and prompts under a window 203 to 204 each; with
+// none or three for few, 64 decodes take 391 and 385 us for 389, but 3 decodes 19.0 and 18.7
+// for 17.9.  Parts of one step or four: 3 decodes 17.2 and 19.4 us, and 64-element heads under
+// a window 22.6 each for 22.2.
 ChunkTiling chunk_tc_tiling() { return {kBM, kQT, kFew, kBN, 5 * kBN, kBN, 2 * kBN, 1}; }
 
 namespace {

@@ -19,8 +19,8 @@ constexpr uint32_t kWherePlan = 9, kWhereAppend = 10;  // status "where" ids
 // exchange between blocks, and the same result in every run.  A page taken from
 // above the old top of the stack is one given back in this call; it is read from
 // the ended request's block table, which no block writes.
-// Latency bound: the launch, two dependent rounds of loads and the scan: 3.4 us for
-// 8 decodes, 6.2 us for 1000 requests with 230 KB of lengths, pages and slots
+// Latency bound: the launch, two dependent rounds of loads and the scan: 3.5 us for
+// 8 decodes, 6.3 us for 1000 requests with 230 KB of lengths, pages and slots
 // (of which a kernel that does nothing takes 2).
 constexpr int kPlanThreads = 512;
 
