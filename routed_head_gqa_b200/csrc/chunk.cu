@@ -263,8 +263,9 @@ __device__ __forceinline__ void take_again(const ChunkGeom& u, const T* Q, const
 #pragma unroll 1
         for (; x.b < u.n_seqs && x.b <= to.b; ++x.b, x.q = x.i = 0) {
             const int t0 = u.cu[x.b], t1 = u.cu[x.b + 1], L = u.lengths[x.b];
-            const ChunkSeq s = {t0, t1 - t0, L};
-            if (t0 < 0 || s.n < 2 || t1 > u.T || L < s.n || L > u.cap || chunk_kind(u, s.n) != kind) continue;
+            const ChunkSeq s = {t0, (int)((unsigned)t1 - (unsigned)t0), L};
+            // no work, one row a unit, or entries that contradict each other (as chunk_seq, which has reported them)
+            if (t0 < 0 || t1 < t0 || t1 > u.T || s.n < 2 || L < s.n || L > u.cap || chunk_kind(u, s.n) != kind) continue;
 #pragma unroll 1
             for (; x.q < u.g; ++x.q, x.i = 0)
 #pragma unroll 1

@@ -94,7 +94,7 @@ struct ChunkSeq {
 // (reported): rows outside the packed tensor, a cache shorter than the new
 // tokens or longer than the block table.
 __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkGeom& u, int b, int t0, int t1, int L) {
-    ChunkSeq s = {t0, t1 - t0, L};
+    ChunkSeq s = {t0, (int)((unsigned)t1 - (unsigned)t0), L};  // of any entries, before they are checked
     if (t0 < 0 || t1 < t0 || t1 > u.T || (s.n > 0 && (L < s.n || L > u.cap))) {
         report_error(u.status, GQE_ERR_INVALID_ARGUMENT, kWhereChunk, (uint32_t)b);
         s.n = 0;

@@ -268,3 +268,31 @@ def test_bad_heads_are_skipped(name, dtype):
     # a bad selection changes nothing else, bit for bit
     clean.run()
     assert torch.equal(st.O[named], clean.O[named])
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(dtype=F32, d=32), dict(k=1, d=64, ps=4)], ids=["bf16", "f32", "bf16 ps4"])
+@pytest.mark.parametrize("ends", [(2 ** 31 - 10, -2 ** 31), (-5, 9), (60, 20), (2 ** 31 - 1, 0)])
+def test_bad_requests_beside_spoilt_rows(kw, ends):
+    """Requests whose row ranges contradict each other (differences of two that wrap to a small length among them) beside
+    some whose rows are taken again: skipped by that as well."""
+    new, ctx = [30, 8, 8, 8, 30], [50, 100, 100, 100, 7]
+    st, clean = Step(U.gqe(), new=new, ctx=ctx, seed=41, **kw), Step(U.gqe(), new=new, ctx=ctx, seed=41, **kw)
+    for b in (0, 4):
+        st.V.view(-1, *st.V.shape[2:])[st.rows_of(b)[-1]] = float("nan")
+    st.cu_d[2], st.cu_d[3] = ends
+    st.run()
+    assert st.status() == st.g.GQE_ERR_INVALID_ARGUMENT
+    sees = torch.zeros_like(st.O, dtype=torch.bool)
+    for b in (0, 4):
+        for q in range(st.idx.shape[1]):
+            sees |= group_rows(st, b, q, [new[b] - 1])
+    # The rows of requests 0 and 4, but for those that a range which does not contradict itself claims as well: a request
+    # between two bad ones may own any rows.
+    cu, T = st.cu_d.tolist(), st.cu[-1]
+    kept = torch.zeros_like(sees)
+    kept[:st.cu[1]] = kept[st.cu[4]:] = True
+    for b in (1, 2, 3):
+        if 0 <= cu[b] <= cu[b + 1] <= T and cu[b + 1] - cu[b] <= st.lengths[b]:
+            kept[cu[b]:cu[b + 1]] = False
+    assert kept.any() and torch.isnan(st.O[kept & sees]).all()
+    assert within(st, clean, kept & ~sees)
